@@ -3,6 +3,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "adapters.h"
 #include "common.cuh"
 #include "ep.h"
 #include "launch.h"
@@ -446,6 +447,170 @@ e4b_status e4b_ep_combine(const uint16_t* ys, int64_t H, const int32_t* inv_perm
   if (!aligned16(ys) || !aligned16(y)) return E4B_ERR_MISALIGNED;
   g_last_launches = 1;
   return cuda_status(launch_ep_combine(ys, H, inv_perm, T, top_k, y, static_cast<cudaStream_t>(stream), sm_count()));
+}
+
+// Row buffers of the adapter path: H values (a multiple of 8) in rows of
+// stride ld, 16-byte aligned.
+static e4b_status check_rows(const void* p, int64_t ld, int64_t H) {
+  if (!p) return E4B_ERR_INVALID_ARG;
+  if (ld < H) return E4B_ERR_INVALID_ARG;
+  if (!aligned16(p) || ld % 8) return E4B_ERR_MISALIGNED;
+  return E4B_OK;
+}
+
+static e4b_status check_slots(int64_t T, int32_t top_k, int64_t H, int64_t R_max) {
+  if (T < 0 || top_k <= 0 || H <= 0 || R_max < 0) return E4B_ERR_INVALID_ARG;
+  if (H % 8 || T >= (int64_t(1) << 31) || T * int64_t(top_k) >= (int64_t(1) << 31) || R_max >= (int64_t(1) << 31))
+    return E4B_ERR_UNSUPPORTED;
+  return E4B_OK;
+}
+
+e4b_status e4b_permute(const uint16_t* x, int64_t ld_x, int64_t T, int64_t H, const int32_t* perm, int32_t top_k,
+                       const int64_t* offsets, int32_t E, int64_t R_max, uint16_t* xs, int64_t ld_xs, void* stream) {
+  e4b_status st = check_slots(T, top_k, H, R_max);
+  if (st != E4B_OK) return st;
+  if (E <= 0) return E4B_ERR_INVALID_ARG;
+  g_last_launches = 0;
+  if (T == 0 || R_max == 0) return E4B_OK;
+  if (!perm || !offsets) return E4B_ERR_INVALID_ARG;
+  if ((st = check_rows(x, ld_x, H)) != E4B_OK || (st = check_rows(xs, ld_xs, H)) != E4B_OK) return st;
+  if (R_max > T * top_k) R_max = T * top_k;  // perm has an entry for every slot
+  g_last_launches = 1;
+  return cuda_status(launch_permute({x, ld_x}, T, H, perm, top_k, offsets, E, R_max, {xs, ld_xs},
+                                    static_cast<cudaStream_t>(stream), sm_count()));
+}
+
+e4b_status e4b_permute_backward(const uint16_t* dxs, int64_t ld_dxs, int64_t R_max, int64_t H,
+                                const int32_t* inv_perm, int64_t T, int32_t top_k, uint16_t* dx, int64_t ld_dx,
+                                void* stream) {
+  return e4b_unpermute(dxs, ld_dxs, R_max, H, inv_perm, nullptr, T, top_k, dx, ld_dx, stream);
+}
+
+e4b_status e4b_unpermute(const uint16_t* ys, int64_t ld_ys, int64_t R_max, int64_t H, const int32_t* inv_perm,
+                         const float* gates, int64_t T, int32_t top_k, uint16_t* y, int64_t ld_y, void* stream) {
+  e4b_status st = check_slots(T, top_k, H, R_max);
+  if (st != E4B_OK) return st;
+  g_last_launches = 0;
+  if (T == 0) return E4B_OK;
+  if (!inv_perm) return E4B_ERR_INVALID_ARG;
+  if (R_max > 0 && (st = check_rows(ys, ld_ys, H)) != E4B_OK) return st;
+  if ((st = check_rows(y, ld_y, H)) != E4B_OK) return st;
+  g_last_launches = 1;
+  return cuda_status(launch_sum_slots({ys, ld_ys}, R_max, H, inv_perm, gates, T, top_k, {y, ld_y},
+                                      static_cast<cudaStream_t>(stream), sm_count()));
+}
+
+e4b_status e4b_unpermute_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* ys, int64_t ld_ys, int64_t R_max,
+                                  int64_t H, const int32_t* inv_perm, const float* gates, int64_t T, int32_t top_k,
+                                  uint16_t* dys, int64_t ld_dys, float* dgates, void* stream) {
+  e4b_status st = check_slots(T, top_k, H, R_max);
+  if (st != E4B_OK) return st;
+  g_last_launches = 0;
+  if (T == 0) return E4B_OK;
+  if (!inv_perm || (!dys && !dgates)) return E4B_ERR_INVALID_ARG;
+  if ((st = check_rows(dy, ld_dy, H)) != E4B_OK) return st;
+  if (R_max > 0 && dgates && (st = check_rows(ys, ld_ys, H)) != E4B_OK) return st;
+  if (dys && (st = check_rows(dys, ld_dys, H)) != E4B_OK) return st;
+  g_last_launches = 1;
+  return cuda_status(launch_unpermute_backward({dy, ld_dy}, {ys, ld_ys}, R_max, H, inv_perm, gates, T, top_k,
+                                               {dys, ld_dys}, dgates, static_cast<cudaStream_t>(stream), sm_count()));
+}
+
+static e4b_status run_glu(const e4b_glu_args* a, bool backward, void* stream) {
+  if (!a || a->I <= 0 || a->R_max < 0 || (a->offsets && a->E <= 0)) return E4B_ERR_INVALID_ARG;
+  e4b_status st = check_variant(a->gate_up_layout, a->activation, a->glu_limit, nullptr, nullptr);
+  if (st != E4B_OK) return st;
+  if (a->I % 8 || a->R_max >= (int64_t(1) << 31) || a->I >= (int64_t(1) << 31)) return E4B_ERR_UNSUPPORTED;
+  g_last_launches = 0;
+  if (a->R_max == 0) return E4B_OK;
+  if ((st = check_rows(a->gu, a->ld_gu, 2 * a->I)) != E4B_OK) return st;
+  if ((!backward || a->h) && (st = check_rows(a->h, a->ld_h, a->I)) != E4B_OK) return st;
+  if (backward && ((st = check_rows(a->dh, a->ld_dh, a->I)) != E4B_OK ||
+                   (st = check_rows(a->dgu, a->ld_dgu, 2 * a->I)) != E4B_OK))
+    return st;
+  if (backward && a->dgu == a->gu && a->ld_dgu != a->ld_gu) return E4B_ERR_INVALID_ARG;
+  g_last_launches = 1;
+  return cuda_status(launch_glu(*a, backward, static_cast<cudaStream_t>(stream), sm_count()));
+}
+
+e4b_status e4b_glu(const e4b_glu_args* args, void* stream) { return run_glu(args, false, stream); }
+
+e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream) { return run_glu(args, true, stream); }
+
+static e4b_status check_lora_sizes(int32_t G, int32_t r, int64_t N, int64_t K, int64_t R_max) {
+  if (G <= 0 || r <= 0 || N <= 0 || K <= 0 || R_max < 0) return E4B_ERR_INVALID_ARG;
+  if (r % 8 || r > kLoraMaxRank || N % 8 || K % 8 || G > 1024) return E4B_ERR_UNSUPPORTED;
+  if (R_max > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return E4B_ERR_UNSUPPORTED;
+  // CTAs are counted in 31 bits: at most one per 128 rows and 256 columns,
+  // plus one per group and 256 columns
+  const int64_t cols = (N > K ? N : K) / 256 + 1;
+  if ((R_max / 32 + G + 1) > (int64_t(1) << 31) / cols) return E4B_ERR_UNSUPPORTED;
+  return E4B_OK;
+}
+
+e4b_status e4b_lora_workspace_size(int32_t G, int32_t r, int64_t N, int64_t K, int64_t R_max, int32_t backward,
+                                   size_t* bytes) {
+  if (!bytes) return E4B_ERR_INVALID_ARG;
+  const e4b_status st = check_lora_sizes(G, r, N, K, R_max);
+  if (st != E4B_OK) return st;
+  *bytes = lora_workspace_bytes(G, r, N, K, R_max, backward != 0, sm_count());
+  return E4B_OK;
+}
+
+// What both directions of e4b_lora ask of their arguments.
+static e4b_status check_lora(const e4b_lora_args* a, void* ws, size_t ws_bytes, bool backward) {
+  if (!a->a || !a->b || !a->offsets || !ws || (a->row && a->rows < 0)) return E4B_ERR_INVALID_ARG;
+  if (!aligned16(a->a) || !aligned16(a->b) || !aligned16(a->s) || !aligned16(a->da) || !aligned16(a->db) ||
+      !aligned16(ws))
+    return E4B_ERR_MISALIGNED;
+  if (ws_bytes < lora_workspace_bytes(a->G, a->r, a->N, a->K, a->R_max, backward, sm_count()))
+    return E4B_ERR_WORKSPACE_TOO_SMALL;
+  return E4B_OK;
+}
+
+e4b_status e4b_lora(const e4b_lora_args* a, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+  if (!a || flags) return E4B_ERR_INVALID_ARG;
+  e4b_status st = check_lora_sizes(a->G, a->r, a->N, a->K, a->R_max);
+  if (st != E4B_OK) return st;
+  if (a->h) {
+    if ((st = check_variant(a->gate_up_layout, a->activation, a->glu_limit, nullptr, nullptr)) != E4B_OK) return st;
+    if (a->N % 16) return E4B_ERR_UNSUPPORTED;
+  }
+  g_last_launches = 0;
+  if (a->R_max == 0) return E4B_OK;
+  if (!a->s && !a->y && !a->h) return E4B_ERR_INVALID_ARG;
+  if ((st = check_lora(a, ws, ws_bytes, false)) != E4B_OK) return st;
+  if ((st = check_rows(a->x, a->ld_x, a->K)) != E4B_OK) return st;
+  if (a->base && (st = check_rows(a->base, a->ld_base, a->N)) != E4B_OK) return st;
+  if (a->y && (st = check_rows(a->y, a->ld_y, a->N)) != E4B_OK) return st;
+  if (a->h && (st = check_rows(a->h, a->ld_h, a->N / 2)) != E4B_OK) return st;
+  if (a->y && a->y == a->base && a->ld_y != a->ld_base) return E4B_ERR_INVALID_ARG;
+  int launches = 0;
+  st = cuda_status(launch_lora(*a, ws, static_cast<cudaStream_t>(stream), sm_count(), &launches));
+  g_last_launches = launches;
+  return st;
+}
+
+e4b_status e4b_lora_backward(const e4b_lora_args* a, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+  if (!a || (flags & ~E4B_FLAG_ACCUMULATE)) return E4B_ERR_INVALID_ARG;
+  e4b_status st = check_lora_sizes(a->G, a->r, a->N, a->K, a->R_max);
+  if (st != E4B_OK) return st;
+  g_last_launches = 0;
+  if (!a->dx && !a->da && !a->db) return E4B_ERR_INVALID_ARG;
+  if ((st = check_lora(a, ws, ws_bytes, true)) != E4B_OK) return st;
+  if (a->R_max > 0) {  // without rows the gradients are still set
+    if ((st = check_rows(a->dy, a->ld_dy, a->N)) != E4B_OK) return st;
+    if (a->da && (st = check_rows(a->x, a->ld_x, a->K)) != E4B_OK) return st;
+    if (a->db && !a->s) return E4B_ERR_INVALID_ARG;
+    if (a->dx_base && (st = check_rows(a->dx_base, a->ld_dx_base, a->K)) != E4B_OK) return st;
+    if (a->dx && (st = check_rows(a->dx, a->ld_dx, a->K)) != E4B_OK) return st;
+    if (a->dx && a->dx == a->dx_base && a->ld_dx != a->ld_dx_base) return E4B_ERR_INVALID_ARG;
+  }
+  int launches = 0;
+  st = cuda_status(launch_lora_backward(*a, (flags & E4B_FLAG_ACCUMULATE) != 0, ws, static_cast<cudaStream_t>(stream),
+                                        sm_count(), &launches));
+  g_last_launches = launches;
+  return st;
 }
 
 // Workspace of the int4-b32 decode path: the status words, then h [top_k, I].

@@ -29,6 +29,7 @@ FLAG_IDS_READY = 0x10  # e4b_gemv_int4_b32: ids and gates not written by the pre
 FLAG_MX_ACT_E4M3 = 0x20  # native MXFP4 path: one e4m3 term per activation (OCP MXFP8 rule)
 FLAG_MX_DECODE = 0x40  # MXFP4 with prepared stacks: the decode-to-bf16 tcgen05 path anyway
 FLAG_TC_SINGLE_SM = 0x80  # large-M projections on the one-SM tcgen05 kernel instead of SM pairs
+FLAG_ACCUMULATE = 0x100  # e4b_lora_backward: add to the adapter gradients
 FLAG_NF4_PRODUCT_DECODE = 0x8  # small-M NF4: bf16(level * absmax) operands (the default is bf16(level), absmax after the block MMA)
 STATUS_NAMES = {
     0: "E4B_OK", 1: "E4B_ERR_INVALID_ARG", 2: "E4B_ERR_UNSUPPORTED",
@@ -47,6 +48,8 @@ EXPORTED = [
     "e4b_quantize_int4_b32", "e4b_gptq_pack_int4_b32", "e4b_gemv_int4_b32",
     "e4b_ep_dest", "e4b_ep_pack", "e4b_ep_combine",
     "e4b_mxfp4_native_size", "e4b_mxfp4_native_prepare", "e4b_quantize_mxfp8",
+    "e4b_permute", "e4b_permute_backward", "e4b_unpermute", "e4b_unpermute_backward",
+    "e4b_glu", "e4b_glu_backward", "e4b_lora_workspace_size", "e4b_lora", "e4b_lora_backward",
 ]
 EPI = {"store": E4B_EPI_STORE, "swiglu": E4B_EPI_SWIGLU, "combine": E4B_EPI_COMBINE}
 
@@ -101,6 +104,30 @@ class Int4GemvArgs(ctypes.Structure):
     ]
 
 
+class GluArgs(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int32), ("gate_up_layout", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("glu_alpha", ctypes.c_float), ("glu_limit", ctypes.c_float), ("I", ctypes.c_int64),
+        ("R_max", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("gu", ctypes.c_void_p), ("ld_gu", ctypes.c_int64),
+        ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64), ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64),
+        ("dgu", ctypes.c_void_p), ("ld_dgu", ctypes.c_int64),
+    ]
+
+
+class LoraArgs(ctypes.Structure):
+    _fields_ = [
+        ("G", ctypes.c_int32), ("r", ctypes.c_int32), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("R_max", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p), ("row", ctypes.c_void_p), ("rows", ctypes.c_int64), ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64), ("s", ctypes.c_void_p), ("base", ctypes.c_void_p), ("ld_base", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+        ("gate_up_layout", ctypes.c_int32), ("activation", ctypes.c_int32), ("glu_alpha", ctypes.c_float),
+        ("glu_limit", ctypes.c_float), ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+        ("dx_base", ctypes.c_void_p), ("ld_dx_base", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p),
+    ]
+
+
 # expert-variant codes (include/e4b.h)
 LAYOUT = {"halves": 0, "interleaved": 1}
 ACT = {"swiglu": 0, "clamped_glu": 1}
@@ -148,6 +175,15 @@ def lib() -> ctypes.CDLL:
         "e4b_mxfp4_native_size": [i32, i64, i64, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)],
         "e4b_mxfp4_native_prepare": [vp, vp, i32, i64, i64, i32, i32, vp, vp, vp],
         "e4b_quantize_mxfp8": [vp, i64, i64, vp, vp, vp],
+        "e4b_permute": [vp, i64, i64, i64, vp, i32, vp, i32, i64, vp, i64, vp],
+        "e4b_permute_backward": [vp, i64, i64, i64, vp, i64, i32, vp, i64, vp],
+        "e4b_unpermute": [vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp],
+        "e4b_unpermute_backward": [vp, i64, vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp],
+        "e4b_glu": [ctypes.POINTER(GluArgs), vp],
+        "e4b_glu_backward": [ctypes.POINTER(GluArgs), vp],
+        "e4b_lora_workspace_size": [i32, i32, i64, i64, i64, i32, ctypes.POINTER(sz)],
+        "e4b_lora": [ctypes.POINTER(LoraArgs), vp, sz, ctypes.c_uint32, vp],
+        "e4b_lora_backward": [ctypes.POINTER(LoraArgs), vp, sz, ctypes.c_uint32, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -383,6 +419,235 @@ def e4b_grouped_gemm(fmt, epilogue, codes, scales, a, offsets, out, *, E, N, K, 
                     _ptr(gates), _ptr(out), out.shape[-1], LAYOUT[layout], ACT[act], alpha, limit,
                     _ptr(bias))
     _check(lib().e4b_grouped_gemm(ctypes.byref(args), flags, _stream(stream)), "e4b_grouped_gemm")
+
+
+# ------------------------------------------- rows by expert, activation, adapters
+# These bindings check shapes, types and devices (ValueError) and run on the
+# tensors' device, on `stream` or that device's current stream. Row buffers may
+# have a row stride (stride(1) == 1).
+def _want(name, t, dtype, *shape, rows=False):
+    """Checks a tensor's type, device and shape (None: any size). Without
+    `rows` it has to be contiguous, with it only its rows."""
+    if not t.is_cuda:
+        raise ValueError("e4b kernels take CUDA tensors")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous() and not (rows and t.stride(1) == 1):
+        raise ValueError(f"{name}: the {'rows have' if rows else 'tensor has'} to be contiguous")
+
+
+def _ld(t):
+    # a single row, or none, may carry any stride
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(name, stream, tensors, *args):
+    """Calls the C entry point `name` on the tensors' one device."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        status = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream(dev) if stream is None else stream
+            status = f(*args, s.cuda_stream)
+    _check(status, name)
+
+
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def e4b_permute(x, perm, offsets, xs, *, top_k, stream=None):
+    """xs[p] = x[perm[p] / top_k] for p < offsets[E] (x [T, H], xs [R_max, H])."""
+    T, H = x.shape
+    _want("x", x, _BF16, T, H, rows=True)
+    _want("xs", xs, _BF16, None, H, rows=True)
+    _want("perm", perm, _I32, T * top_k)
+    _want("offsets", offsets, _I64, None)
+    if xs.shape[0] > T * top_k:
+        raise ValueError("xs has more rows than there are slots")
+    _on_device("e4b_permute", stream, (x, perm, offsets, xs), _addr(x), _ld(x), T, H, _addr(perm), top_k,
+               _addr(offsets), offsets.numel() - 1, xs.shape[0], _addr(xs), _ld(xs))
+
+
+def e4b_permute_backward(dxs, inv_perm, dx, *, top_k, stream=None):
+    """dx[t] = the sum of its slots' rows of dxs (dxs [R_max, H], dx [T, H])."""
+    T, H = dx.shape
+    _want("dx", dx, _BF16, T, H, rows=True)
+    _want("dxs", dxs, _BF16, None, H, rows=True)
+    _want("inv_perm", inv_perm, _I32, T * top_k)
+    _on_device("e4b_permute_backward", stream, (dxs, inv_perm, dx), _addr(dxs), _ld(dxs), dxs.shape[0], H,
+               _addr(inv_perm), T, top_k, _addr(dx), _ld(dx))
+
+
+def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
+    """y[t] = the gate-weighted sum of its slots' rows of ys (ys [R_max, H],
+    gates fp32 [T, top_k] or None, y [T, H])."""
+    T, H = y.shape
+    _want("y", y, _BF16, T, H, rows=True)
+    _want("ys", ys, _BF16, None, H, rows=True)
+    _want("inv_perm", inv_perm, _I32, T * top_k)
+    if gates is not None:
+        _want("gates", gates, _F32, T, top_k)
+    _on_device("e4b_unpermute", stream, (ys, inv_perm, gates, y), _addr(ys), _ld(ys), ys.shape[0], H,
+               _addr(inv_perm), _addr(gates), T, top_k, _addr(y), _ld(y))
+
+
+def e4b_unpermute_backward(dy, ys, inv_perm, gates, dys, dgates, *, top_k, stream=None):
+    """dys[inv_perm[s]] = gates[s] dy[t] and dgates[s] = <dy[t], ys[inv_perm[s]]>;
+    dys or dgates may be None, and ys where dgates is."""
+    T, H = dy.shape
+    _want("dy", dy, _BF16, T, H, rows=True)
+    _want("inv_perm", inv_perm, _I32, T * top_k)
+    if gates is not None:
+        _want("gates", gates, _F32, T, top_k)
+    rows = [t for t in (ys, dys) if t is not None]
+    if not rows or (dgates is not None and ys is None):
+        raise ValueError("ys is needed for dgates, dys or dgates for a result")
+    for name, t in (("ys", ys), ("dys", dys)):
+        if t is not None:
+            _want(name, t, _BF16, rows[0].shape[0], H, rows=True)
+    if dgates is not None:
+        _want("dgates", dgates, _F32, T, top_k)
+    _on_device("e4b_unpermute_backward", stream, (dy, ys, inv_perm, gates, dys, dgates), _addr(dy), _ld(dy),
+               _addr(ys), 0 if ys is None else _ld(ys), rows[0].shape[0], H, _addr(inv_perm), _addr(gates), T, top_k,
+               _addr(dys), 0 if dys is None else _ld(dys), _addr(dgates))
+
+
+def _glu_args(gu, offsets, layout, act, alpha, limit):
+    R, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu: rows of 2I values")
+    _want("gu", gu, _BF16, R, I2, rows=True)
+    a = GluArgs(0, LAYOUT[layout], ACT[act], alpha, limit, I2 // 2, R)
+    if offsets is not None:
+        _want("offsets", offsets, _I64, None)
+        a.E, a.offsets = offsets.numel() - 1, _addr(offsets)
+    a.gu, a.ld_gu = _addr(gu), _ld(gu)
+    return a, R, I2 // 2
+
+
+def e4b_glu(gu, h, *, offsets=None, layout="halves", act="swiglu", alpha=1.702, limit=7.0, stream=None):
+    """h = the gated activation of stored gate_up rows (gu [R_max, 2I], h
+    [R_max, I]); with offsets only of the rows p < offsets[E]."""
+    a, R, I = _glu_args(gu, offsets, layout, act, alpha, limit)
+    _want("h", h, _BF16, R, I, rows=True)
+    a.h, a.ld_h = _addr(h), _ld(h)
+    _on_device("e4b_glu", stream, (gu, h, offsets), ctypes.byref(a))
+
+
+def e4b_glu_backward(dh, gu, dgu, *, h=None, offsets=None, layout="halves", act="swiglu", alpha=1.702, limit=7.0,
+                     stream=None):
+    """dgu = the gradient of e4b_glu for dh; dgu may be gu. With h the
+    activation itself is written again too."""
+    a, R, I = _glu_args(gu, offsets, layout, act, alpha, limit)
+    _want("dh", dh, _BF16, R, I, rows=True)
+    _want("dgu", dgu, _BF16, R, 2 * I, rows=True)
+    a.dh, a.ld_dh, a.dgu, a.ld_dgu = _addr(dh), _ld(dh), _addr(dgu), _ld(dgu)
+    if h is not None:
+        _want("h", h, _BF16, R, I, rows=True)
+        a.h, a.ld_h = _addr(h), _ld(h)
+    _on_device("e4b_glu_backward", stream, (dh, gu, dgu, h, offsets), ctypes.byref(a))
+
+
+def e4b_lora_workspace_size(G, r, N, K, R_max, backward=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().e4b_lora_workspace_size(G, r, N, K, R_max, int(backward), ctypes.byref(n)),
+           "e4b_lora_workspace_size")
+    return n.value
+
+
+def _lora_args(a, b, offsets, scale, row, R_max, rows):
+    """The part of the arguments both directions share. rows: the tensors
+    [rows, *] that positions point into."""
+    G, r, K = a.shape
+    N = b.shape[1] if b.dim() == 3 else -1
+    _want("a", a, _BF16, G, r, K)
+    _want("b", b, _BF16, G, N, r)
+    _want("offsets", offsets, _I64, G + 1)
+    if scale is not None:
+        _want("scale", scale, _F32, G)
+    n = rows[0][1].shape[0]
+    for name, t, width in rows:
+        _want(name, t, _BF16, n, width(N, K), rows=True)
+    if row is not None:
+        _want("row", row, _I32, R_max)
+    elif n != R_max:
+        raise ValueError(f"{rows[0][0]}: expected {R_max} rows, got {n}")
+    return LoraArgs(G, r, N, K, R_max, _addr(a), _addr(b), _addr(scale), _addr(offsets), _addr(row), n)
+
+
+def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=None, row=None, layout="halves",
+             act="swiglu", alpha=1.702, limit=7.0, stream=None):
+    """s[p] = A_g x[i], y[i] = base[i] + scale[g] B_g s[p] and h = act(y) for the
+    positions p of every group g, i = row[p] (p without row); of s, y and h
+    those that are given are written. a [G, r, K], b [G, N, r], x [*, K], base
+    and y [*, N], h [*, N/2], s fp32 [R_max, r], scale fp32 [G], row [R_max]."""
+    R_max = row.numel() if row is not None else x.shape[0]
+    rows = [("x", x, lambda N, K: K)]
+    rows += [(n, t, lambda N, K: N) for n, t in (("base", base), ("y", y)) if t is not None]
+    rows += [("h", h, lambda N, K: N // 2)] if h is not None else []
+    p = _lora_args(a, b, offsets, scale, row, R_max, rows)
+    p.x, p.ld_x = _addr(x), _ld(x)
+    if s is not None:
+        _want("s", s, _F32, R_max, p.r)
+        p.s = _addr(s)
+    if base is not None:
+        p.base, p.ld_base = _addr(base), _ld(base)
+    if y is not None:
+        p.y, p.ld_y = _addr(y), _ld(y)
+    if h is not None:
+        p.h, p.ld_h = _addr(h), _ld(h)
+        p.gate_up_layout, p.activation, p.glu_alpha, p.glu_limit = LAYOUT[layout], ACT[act], alpha, limit
+    _want("ws", ws, torch.uint8, None)
+    _on_device("e4b_lora", stream, (x, a, b, offsets, ws, base, y, h, s, scale, row), ctypes.byref(p), _addr(ws),
+               ws.numel(), 0)
+
+
+def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=None, db=None, accumulate=False,
+                      scale=None, row=None, stream=None):
+    """The gradients of e4b_lora for dy [*, N]: dx[i] = dx_base[i] + A_g^T t[p],
+    da[g] = sum_p t[p] x[i]^T and db[g] = scale[g] sum_p dy[i] s[p]^T with t[p] =
+    scale[g] B_g^T dy[i]; those of dx, da (fp32 [G, r, K]) and db (fp32 [G, N, r])
+    that are given. accumulate: da and db are added to. x may be None without
+    da, s without db."""
+    R_max = row.numel() if row is not None else dy.shape[0]
+    rows = [("dy", dy, lambda N, K: N)]
+    rows += [(n, t, lambda N, K: K) for n, t in (("x", x), ("dx", dx), ("dx_base", dx_base)) if t is not None]
+    p = _lora_args(a, b, offsets, scale, row, R_max, rows)
+    p.dy, p.ld_dy = _addr(dy), _ld(dy)
+    if x is not None:
+        p.x, p.ld_x = _addr(x), _ld(x)
+    if s is not None:
+        _want("s", s, _F32, R_max, p.r)
+        p.s = _addr(s)
+    if dx is not None:
+        p.dx, p.ld_dx = _addr(dx), _ld(dx)
+    if dx_base is not None:
+        p.dx_base, p.ld_dx_base = _addr(dx_base), _ld(dx_base)
+    if da is not None:
+        _want("da", da, _F32, p.G, p.r, p.K)
+        p.da = _addr(da)
+    if db is not None:
+        _want("db", db, _F32, p.G, p.N, p.r)
+        p.db = _addr(db)
+    _want("ws", ws, torch.uint8, None)
+    _on_device("e4b_lora_backward", stream, (dy, a, b, offsets, ws, x, s, dx, dx_base, da, db, scale, row),
+               ctypes.byref(p), _addr(ws), ws.numel(), FLAG_ACCUMULATE if accumulate else 0)
 
 
 # ---------------------------------------------------------------- the layer

@@ -480,6 +480,154 @@ e4b_status e4b_ep_pack(const uint16_t* x, int64_t H, const int32_t* ids, const f
 e4b_status e4b_ep_combine(const uint16_t* ys, int64_t H, const int32_t* inv_perm, int64_t T, int32_t top_k,
                           uint16_t* y, void* stream);
 
+/* --------------------------------------- token rows by expert and back */
+/*
+ * The steps around e4b_grouped_gemm / e4b_grouped_dgrad for callers that run
+ * the layer projection by projection (a training step, adapters between the
+ * projections), on the arrays of e4b_route: slot s = t * top_k + j, perm[p] = s,
+ * inv_perm[s] = p (-1: dropped). Rows are bf16, H % 8 == 0, 16-byte aligned,
+ * with a stride (ld_*, in values) of at least H that is a multiple of 8. A
+ * slot or position outside the given sizes is treated as dropped. Sums run in
+ * fp32 in slot order and are rounded once, so repeated calls give the same
+ * bits. T == 0 or R_max == 0 is a no-op. T * top_k < 2^31. No output may
+ * overlap an input.
+ */
+
+/* xs[p] = x[perm[p] / top_k] for p < min(offsets[E], R_max); the other rows of
+ * xs [R_max, H] are left as they were. */
+e4b_status e4b_permute(const uint16_t* x, int64_t ld_x, int64_t T, int64_t H, const int32_t* perm, int32_t top_k,
+                       const int64_t* offsets, int32_t E, int64_t R_max, uint16_t* xs, int64_t ld_xs, void* stream);
+
+/* dx[t] = bf16(sum_j dxs[inv_perm[t, j]]), the gradient of e4b_permute; a token
+ * whose slots were all dropped gets 0. dxs [R_max, H], dx [T, H]. */
+e4b_status e4b_permute_backward(const uint16_t* dxs, int64_t ld_dxs, int64_t R_max, int64_t H,
+                                const int32_t* inv_perm, int64_t T, int32_t top_k, uint16_t* dx, int64_t ld_dx,
+                                void* stream);
+
+/* y[t] = bf16(sum_j gates[t, j] ys[inv_perm[t, j]]); gates fp32 [T, top_k], or
+ * NULL for weights of 1. A dropped slot adds nothing (its gate is not read).
+ * ys [R_max, H], y [T, H]. */
+e4b_status e4b_unpermute(const uint16_t* ys, int64_t ld_ys, int64_t R_max, int64_t H, const int32_t* inv_perm,
+                         const float* gates, int64_t T, int32_t top_k, uint16_t* y, int64_t ld_y, void* stream);
+
+/* The gradients of e4b_unpermute: dys[inv_perm[s]] = bf16(gates[s] dy[t]) and
+ * dgates[s] = <dy[t], ys[inv_perm[s]]> (fp32; 0 for a dropped slot). dys or
+ * dgates may be NULL (not both); ys is read for dgates only and may be NULL
+ * without it. Rows of dys [R_max, H] that belong to no slot are left as they
+ * were. */
+e4b_status e4b_unpermute_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* ys, int64_t ld_ys, int64_t R_max,
+                                  int64_t H, const int32_t* inv_perm, const float* gates, int64_t T, int32_t top_k,
+                                  uint16_t* dys, int64_t ld_dys, float* dgates, void* stream);
+
+/* ------------------------------------------------------ gated activation */
+/*
+ * The gated activation of e4b_moe_weights on stored gate_up rows, and its
+ * gradient. gu bf16 [R_max, 2I] in the rows' gate_up_layout; the rows
+ * p < R are computed, R = min(offsets[E], R_max), or R_max with offsets NULL;
+ * the other rows of the outputs are left as they were.
+ *   e4b_glu           h[p] = bf16(act(gu[p])), bf16 [R_max, I] (dh, dgu unused)
+ *   e4b_glu_backward  dgu[p] = bf16(dh[p] * d act), in gu's layout, and, where
+ *                     h is not NULL, h[p] again (so that the forward pass need
+ *                     not keep it). The clamps pass a gradient up to and
+ *                     including the limit. dgu may be gu (in place); no other
+ *                     overlap is allowed.
+ * I % 8 == 0; strides (in values) multiples of 8, of at least 2I (gu, dgu) and
+ * I (h, dh); pointers 16-byte aligned.
+ */
+typedef struct {
+  int32_t E;               /* offsets has E + 1 entries (unused without offsets) */
+  int32_t gate_up_layout;  /* e4b_gate_up_layout */
+  int32_t activation;      /* e4b_activation */
+  float glu_alpha, glu_limit;
+  int64_t I, R_max;
+  const int64_t* offsets;  /* [E+1] or NULL */
+  const uint16_t* gu;
+  int64_t ld_gu;
+  uint16_t* h;
+  int64_t ld_h;
+  const uint16_t* dh;
+  int64_t ld_dh;
+  uint16_t* dgu;
+  int64_t ld_dgu;
+} e4b_glu_args;
+
+e4b_status e4b_glu(const e4b_glu_args* args, void* stream);
+e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
+
+/* ------------------------------------------------------ low-rank adapters */
+/*
+ * Low-rank adapters of G groups of rows beside a shared projection: one adapter
+ * per expert on its routed rows ("experts4bit-qlora" README: adapters on frozen
+ * 4-bit experts), or one per request on a batch. Positions p of group g are
+ * [offsets[g], offsets[g+1]), at most R_max in all; row i = row ? row[p] : p
+ * (rows of a position order, or any order through the map of e4b_route). With
+ * A_g = a[g] [r, K], B_g = b[g] [N, r], w_g = scale ? scale[g] : 1:
+ *   e4b_lora           s[p] = A_g x[i]
+ *                      y32 = base[i] + w_g B_g s[p]  (base NULL: 0)
+ *                      y[i] = bf16(y32);  h[i] = bf16(act(y32)) as in e4b_glu
+ *     of s, y and h those that are not NULL are written (one at least). h needs
+ *     N = 2I with the gate_up layout, N % 16 == 0.
+ *   e4b_lora_backward  t[p] = w_g B_g^T dy[i]
+ *                      dx[i] = bf16(dx_base[i] + A_g^T t[p])  (dx_base NULL: 0)
+ *                      da[g] = sum_p t[p] x[i]^T,  db[g] = w_g sum_p dy[i] s[p]^T
+ *     of dx, da and db those that are not NULL are written (one at least); x is
+ *     read for da, s (as e4b_lora wrote it) for db. da [G, r, K] and db
+ *     [G, N, r] are fp32; a group without rows gets zeros. With
+ *     E4B_FLAG_ACCUMULATE the gradients are added to what da and db hold.
+ * x, dx, dx_base [*, K] and y, base, dy [*, N], h [*, N/2]: bf16 rows, strides
+ * (in values) multiples of 8. s fp32 [R_max, r], by position. y may be base and
+ * dx may be dx_base (in place); no other output may overlap an input. row: the
+ * rows of two positions must differ; an entry outside [0, rows) leaves its
+ * position out (s[p] = 0, no row written, nothing added to the gradients).
+ * Rows of no position are left as they were.
+ * fp32 accumulation; s and t enter the second product as two bf16 terms (16
+ * bits of mantissa); every reduction runs in a fixed order, so repeated calls
+ * give the same bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
+ * with zeros; an adapter of a higher rank is the sum of two, the second with
+ * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max <= 2^30;
+ * all pointers but offsets, row and scale 16-byte aligned. ws: device scratch of
+ * e4b_lora_workspace_size bytes (16-byte aligned), for one call at a time.
+ * Launches: 2 forward, up to 4 backward.
+ */
+#define E4B_FLAG_ACCUMULATE 0x100u /* e4b_lora_backward: add to da and db */
+
+typedef struct {
+  int32_t G, r;
+  int64_t N, K, R_max;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;      /* [G] or NULL */
+  const int64_t* offsets;  /* [G+1] */
+  const int32_t* row;      /* [R_max] or NULL */
+  int64_t rows;            /* rows of x, y ... that row points into (unused without row) */
+  const uint16_t* x;
+  int64_t ld_x;
+  float* s;                /* e4b_lora: output; e4b_lora_backward: input */
+  const uint16_t* base;    /* forward */
+  int64_t ld_base;
+  uint16_t* y;
+  int64_t ld_y;
+  uint16_t* h;
+  int64_t ld_h;
+  int32_t gate_up_layout;  /* with h, as in e4b_moe_weights */
+  int32_t activation;
+  float glu_alpha, glu_limit;
+  const uint16_t* dy;      /* backward */
+  int64_t ld_dy;
+  const uint16_t* dx_base;
+  int64_t ld_dx_base;
+  uint16_t* dx;
+  int64_t ld_dx;
+  float* da;
+  float* db;
+} e4b_lora_args;
+
+/* Host: workspace bytes of e4b_lora (backward == 0) or e4b_lora_backward. */
+e4b_status e4b_lora_workspace_size(int32_t G, int32_t r, int64_t N, int64_t K, int64_t R_max, int32_t backward,
+                                   size_t* bytes);
+e4b_status e4b_lora(const e4b_lora_args* args, void* ws, size_t ws_bytes, uint32_t flags, void* stream);
+e4b_status e4b_lora_backward(const e4b_lora_args* args, void* ws, size_t ws_bytes, uint32_t flags, void* stream);
+
 /* ---------------------------------------------------------- whole layer */
 
 /* Host: workspace bytes for e4b_moe_forward with T tokens and top_k slots.
