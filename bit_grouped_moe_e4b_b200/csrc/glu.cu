@@ -34,7 +34,11 @@ E4B_DEV uint4 pack8(const float (&a)[8]) {
 // The hardware exp2 and reciprocal (relative error ~2^-20, far below bf16's
 // half step). Below -87 the reciprocal flushes to zero, where the exact value
 // is under 2^-125.
-E4B_DEV float fast_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+E4B_DEV float fast_sigmoid(float v) {
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + __expf(-v)));
+  return s;
+}
 
 struct GluRows {
   const uint16_t* gu;
@@ -46,104 +50,147 @@ struct GluRows {
   uint16_t* dgu;
   int64_t ld_dgu;
   int64_t I;
-  int act;
   float alpha, limit;
 };
 
-// Eight pairs of a row. gu is read before dgu is written, element for element
-// by the same thread, so dgu may be gu.
-template <bool INTERLEAVED, bool BACKWARD>
-E4B_DEV void glu_vec(const GluRows& a, int64_t row, int64_t v) {
-  float g[8], u[8];
-  const uint16_t* src = a.gu + row * a.ld_gu;
-  if constexpr (INTERLEAVED) {
-    float w[16];
-    const uint4 lo = reinterpret_cast<const uint4*>(src)[2 * v], hi = reinterpret_cast<const uint4*>(src)[2 * v + 1];
-    unpack8(lo, reinterpret_cast<float(&)[8]>(w[0]));
-    unpack8(hi, reinterpret_cast<float(&)[8]>(w[8]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      g[i] = w[2 * i];
-      u[i] = w[2 * i + 1];
-    }
-  } else {
-    unpack8(reinterpret_cast<const uint4*>(src)[v], g);
-    unpack8(reinterpret_cast<const uint4*>(src + a.I)[v], u);
-  }
-  float h[8];
-  if constexpr (!BACKWARD) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = glu_act(a.act, g[i], u[i], a.alpha, a.limit);
-    reinterpret_cast<uint4*>(a.h + row * a.ld_h)[v] = pack8(h);
-  } else {
-    float d[8], dg[8], du[8];
-    unpack8(reinterpret_cast<const uint4*>(a.dh + row * a.ld_dh)[v], d);
-    const bool clamped = a.act == E4B_ACT_CLAMPED_GLU;
-    const float b = clamped ? a.alpha : 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // comparisons that let NaN inputs through as NaN
-      const bool gout = clamped && g[i] > a.limit;
-      const bool uout = clamped && (u[i] > a.limit || u[i] < -a.limit);
-      const float gc = gout ? a.limit : g[i];
-      const float uc = clamped ? (uout ? copysignf(a.limit, u[i]) : u[i]) + 1.f : u[i];
-      const float sg = fast_sigmoid(b * gc);
-      const float f = gc * sg;
-      h[i] = f * uc;
-      dg[i] = gout ? 0.f : d[i] * uc * (sg * fmaf(b * gc, 1.f - sg, 1.f));
-      du[i] = uout ? 0.f : d[i] * f;
-    }
-    uint16_t* dst = a.dgu + row * a.ld_dgu;
-    if constexpr (INTERLEAVED) {
-      float w[16];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[2 * i] = dg[i];
-        w[2 * i + 1] = du[i];
-      }
-      reinterpret_cast<uint4*>(dst)[2 * v] = pack8(reinterpret_cast<float(&)[8]>(w[0]));
-      reinterpret_cast<uint4*>(dst)[2 * v + 1] = pack8(reinterpret_cast<float(&)[8]>(w[8]));
-    } else {
-      reinterpret_cast<uint4*>(dst)[v] = pack8(dg);
-      reinterpret_cast<uint4*>(dst + a.I)[v] = pack8(du);
-    }
-    if (a.h) reinterpret_cast<uint4*>(a.h + row * a.ld_h)[v] = pack8(h);
-  }
+template <typename T>
+E4B_DEV void put(void* p, T v) {
+  *reinterpret_cast<T*>(p) = v;
 }
 
-// Threads walk the rows' vectors in one flat order; (row, vector) advance by
-// the grid's stride without a division (stride = step_row * V + step_vec).
-template <bool INTERLEAVED, bool BACKWARD>
-__global__ void __launch_bounds__(kGluThreads)
+// A lane's pairs of a row: eight (16 bytes of gates, 16 of ups) with the gate
+// and up halves apart, four (16 bytes of pairs) where they alternate, so that
+// every access of a warp covers whole lines.
+template <bool INTERLEAVED>
+constexpr int kPairs = INTERLEAVED ? 4 : 8;
+
+template <bool INTERLEAVED, bool BACKWARD, bool CLAMPED>
+struct GluVec {
+  uint4 a, b;   // gates and ups, or (a alone) pairs
+  uint4 d;      // dh (interleaved: x, y)
+  __device__ __forceinline__ void load(const GluRows& r, int64_t row, int64_t v) {
+    const uint16_t* src = r.gu + row * r.ld_gu;
+    a = reinterpret_cast<const uint4*>(src)[v];
+    if constexpr (!INTERLEAVED) b = reinterpret_cast<const uint4*>(src + r.I)[v];
+    if constexpr (BACKWARD) {
+      const uint16_t* dh = r.dh + row * r.ld_dh;
+      if constexpr (INTERLEAVED) {
+        const uint2 w = reinterpret_cast<const uint2*>(dh)[v];
+        d = make_uint4(w.x, w.y, 0, 0);
+      } else {
+        d = reinterpret_cast<const uint4*>(dh)[v];
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(const GluRows& r, int64_t row, int64_t v) const {
+    constexpr int P = kPairs<INTERLEAVED>;
+    float g[P], u[P], h[P];
+    if constexpr (INTERLEAVED) {
+      const uint32_t q[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        g[i] = __uint_as_float(q[i] << 16);
+        u[i] = __uint_as_float(q[i] & 0xFFFF0000u);
+      }
+    } else {
+      unpack8(a, g);
+      unpack8(b, u);
+    }
+    if constexpr (!BACKWARD) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) h[i] = glu_act(CLAMPED ? E4B_ACT_CLAMPED_GLU : E4B_ACT_SWIGLU, g[i], u[i], r.alpha, r.limit);
+    } else {
+      float dw[8], dg[P], du[P];
+      unpack8(d, dw);
+      const float slope = CLAMPED ? r.alpha : 1.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        // comparisons that let NaN inputs through as NaN
+        const bool gout = CLAMPED && g[i] > r.limit;
+        const bool uout = CLAMPED && (u[i] > r.limit || u[i] < -r.limit);
+        const float gc = gout ? r.limit : g[i];
+        const float uc = CLAMPED ? (uout ? copysignf(r.limit, u[i]) : u[i]) + 1.f : u[i];
+        const float sg = fast_sigmoid(slope * gc);
+        const float f = gc * sg;
+        h[i] = f * uc;
+        dg[i] = gout ? 0.f : dw[i] * uc * (sg * fmaf(slope * gc, 1.f - sg, 1.f));
+        du[i] = uout ? 0.f : dw[i] * f;
+      }
+      uint16_t* dst = r.dgu + row * r.ld_dgu;
+      if constexpr (INTERLEAVED) {
+        put(reinterpret_cast<uint4*>(dst) + v, make_uint4(pack_bf16x2(dg[0], du[0]), pack_bf16x2(dg[1], du[1]),
+                                                          pack_bf16x2(dg[2], du[2]), pack_bf16x2(dg[3], du[3])));
+      } else {
+        put(reinterpret_cast<uint4*>(dst) + v, pack8(dg));
+        put(reinterpret_cast<uint4*>(dst + r.I) + v, pack8(du));
+      }
+    }
+    if (!BACKWARD || r.h) {
+      uint16_t* dst = r.h + row * r.ld_h;
+      if constexpr (INTERLEAVED)
+        put(reinterpret_cast<uint2*>(dst) + v, make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])));
+      else
+        put(reinterpret_cast<uint4*>(dst) + v, pack8(h));
+    }
+  }
+};
+
+// Threads walk the rows' vectors in one flat order, kUnroll of them in flight;
+// (row, vector) advance by the grid's stride without a division (stride =
+// step_row * V + step_vec). A vector of gu is read before the same vector of
+// dgu is written, by the same thread, so dgu may be gu. Two vectors a thread:
+// 8192 rows of 14336 pairs take 107 us (the copy rate; one vector 125 us, four
+// 121 us), and the gradient with h of 32764 clamped, alternating rows of 2880
+// pairs 189 us (6.0 TB/s, 91% of the copy rate).
+constexpr int kUnroll = 2;
+
+template <bool INTERLEAVED, bool BACKWARD, bool CLAMPED>
+__global__ void __launch_bounds__(kGluThreads, 2)
 glu_kernel(GluRows a, int64_t V, int64_t step_row, int64_t step_vec, const int64_t* __restrict__ offsets,
            int32_t E, int64_t R_max) {
   const int64_t R = offsets ? min(offsets[E], R_max) : R_max;
   const int64_t i = int64_t(blockIdx.x) * kGluThreads + threadIdx.x;
   int64_t row = i / V, v = i - row * V;
   while (row < R) {
-    glu_vec<INTERLEAVED, BACKWARD>(a, row, v);
-    row += step_row;
-    v += step_vec;
-    if (v >= V) {
-      v -= V;
-      ++row;
+    GluVec<INTERLEAVED, BACKWARD, CLAMPED> w[kUnroll];
+    int64_t rows[kUnroll], vs[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      rows[k] = row;
+      vs[k] = v;
+      if (row < R) w[k].load(a, row, v);
+      row += step_row;
+      v += step_vec;
+      if (v >= V) {
+        v -= V;
+        ++row;
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (rows[k] < R) w[k].finish(a, rows[k], vs[k]);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_glu(const e4b_glu_args& a, bool backward, cudaStream_t st, int sms) {
-  GluRows k{a.gu, a.ld_gu, a.dh, a.ld_dh, a.h, a.ld_h, a.dgu, a.ld_dgu, a.I, a.activation, a.glu_alpha, a.glu_limit};
-  const int64_t V = a.I / 8;
+  GluRows k{a.gu, a.ld_gu, a.dh, a.ld_dh, a.h, a.ld_h, a.dgu, a.ld_dgu, a.I, a.glu_alpha, a.glu_limit};
+  const bool il = a.gate_up_layout == E4B_GATE_UP_INTERLEAVED;
+  const int64_t V = a.I / (il ? kPairs<true> : kPairs<false>);
   int64_t grid = (a.R_max * V + kGluThreads - 1) / kGluThreads;
-  const int64_t cap = int64_t(sms) * 8;
+  const int64_t cap = int64_t(sms) * 32;
   if (grid > cap) grid = cap;
   const int64_t stride = grid * kGluThreads;
   const int64_t sr = stride / V, sv = stride % V;
-  const bool il = a.gate_up_layout == E4B_GATE_UP_INTERLEAVED;
-  auto kernel = il ? (backward ? glu_kernel<true, true> : glu_kernel<true, false>)
-                   : (backward ? glu_kernel<false, true> : glu_kernel<false, false>);
+  const bool clamped = a.activation == E4B_ACT_CLAMPED_GLU;
+  using Kernel = void (*)(GluRows, int64_t, int64_t, int64_t, const int64_t*, int32_t, int64_t);
+  static constexpr Kernel kernels[2][2][2] = {
+      {{glu_kernel<false, false, false>, glu_kernel<false, false, true>},
+       {glu_kernel<false, true, false>, glu_kernel<false, true, true>}},
+      {{glu_kernel<true, false, false>, glu_kernel<true, false, true>},
+       {glu_kernel<true, true, false>, glu_kernel<true, true, true>}}};
+  const Kernel kernel = kernels[il][backward][clamped];
   kernel<<<int(grid), kGluThreads, 0, st>>>(k, V, sr, sv, a.offsets, a.E, a.R_max);
   return cudaGetLastError();
 }

@@ -424,144 +424,149 @@ def e4b_grouped_gemm(fmt, epilogue, codes, scales, a, offsets, out, *, E, N, K, 
 # ------------------------------------------- rows by expert, activation, adapters
 # These bindings check shapes, types and devices (ValueError) and run on the
 # tensors' device, on `stream` or that device's current stream. Row buffers may
-# have a row stride (stride(1) == 1).
-def _want(name, t, dtype, *shape, rows=False):
-    """Checks a tensor's type, device and shape (None: any size). Without
-    `rows` it has to be contiguous, with it only its rows."""
+# have a row stride (stride(1) == 1). They are on the path of single tokens, so
+# a check that holds costs one comparison of each property.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+def _refuse(name, t, dtype, shape, dev, rows):
     if not t.is_cuda:
         raise ValueError("e4b kernels take CUDA tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous() and not (rows and t.stride(1) == 1):
-        raise ValueError(f"{name}: the {'rows have' if rows else 'tensor has'} to be contiguous")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: the {'rows have' if rows else 'tensor has'} to be contiguous")
 
 
-def _ld(t):
-    # a single row, or none, may carry any stride
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+def _vec(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of this type and shape on device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+        _refuse(name, t, dtype, shape, dev, False)
+    return t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _rows(name, t, n, width, dev):
+    """(address, row stride) of bf16 rows [n, width] on device dev."""
+    if t.dtype is not _BF16 or t.shape != (n, width) or t.get_device() != dev or dev < 0:
+        _refuse(name, t, _BF16, (n, width), dev, True)
+    if n < 2:  # a single row, or none, may carry any stride
+        ld = -(-width // 8) * 8
+        if n and t.stride(1) != 1 and width > 1:
+            _refuse(name, t, _BF16, (n, width), dev, True)
+        return t.data_ptr(), ld
+    ld, one = t.stride()
+    if one != 1 and width > 1:
+        _refuse(name, t, _BF16, (n, width), dev, True)
+    return t.data_ptr(), ld
 
 
-def _on_device(name, stream, tensors, *args):
-    """Calls the C entry point `name` on the tensors' one device."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        status = f(*args, s.cuda_stream)
+def _matrix(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected rows, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _call(name, dev, stream, *args):
+    """The C entry point `name` on device dev, on `stream` or its current one."""
+    f = getattr(_lib or lib(), name)
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(dev)
+    else:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream(dev) if stream is None else stream
-            status = f(*args, s.cuda_stream)
-    _check(status, name)
-
-
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+            status = f(*args, s)
+    if status:
+        raise E4BError(status, name)
 
 
 def e4b_permute(x, perm, offsets, xs, *, top_k, stream=None):
     """xs[p] = x[perm[p] / top_k] for p < offsets[E] (x [T, H], xs [R_max, H])."""
-    T, H = x.shape
-    _want("x", x, _BF16, T, H, rows=True)
-    _want("xs", xs, _BF16, None, H, rows=True)
-    _want("perm", perm, _I32, T * top_k)
-    _want("offsets", offsets, _I64, None)
-    if xs.shape[0] > T * top_k:
+    T, H = _matrix("x", x)
+    R, dev = _matrix("xs", xs)[0], x.get_device()
+    if R > T * top_k:
         raise ValueError("xs has more rows than there are slots")
-    _on_device("e4b_permute", stream, (x, perm, offsets, xs), _addr(x), _ld(x), T, H, _addr(perm), top_k,
-               _addr(offsets), offsets.numel() - 1, xs.shape[0], _addr(xs), _ld(xs))
+    E = offsets.numel() - 1
+    _call("e4b_permute", dev, stream, *_rows("x", x, T, H, dev), T, H, _vec("perm", perm, _I32, (T * top_k,), dev),
+          top_k, _vec("offsets", offsets, _I64, (E + 1,), dev), E, R, *_rows("xs", xs, R, H, dev))
 
 
 def e4b_permute_backward(dxs, inv_perm, dx, *, top_k, stream=None):
     """dx[t] = the sum of its slots' rows of dxs (dxs [R_max, H], dx [T, H])."""
-    T, H = dx.shape
-    _want("dx", dx, _BF16, T, H, rows=True)
-    _want("dxs", dxs, _BF16, None, H, rows=True)
-    _want("inv_perm", inv_perm, _I32, T * top_k)
-    _on_device("e4b_permute_backward", stream, (dxs, inv_perm, dx), _addr(dxs), _ld(dxs), dxs.shape[0], H,
-               _addr(inv_perm), T, top_k, _addr(dx), _ld(dx))
+    T, H = _matrix("dx", dx)
+    R, dev = _matrix("dxs", dxs)[0], dx.get_device()
+    _call("e4b_permute_backward", dev, stream, *_rows("dxs", dxs, R, H, dev), R, H,
+          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev), T, top_k, *_rows("dx", dx, T, H, dev))
 
 
 def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
     """y[t] = the gate-weighted sum of its slots' rows of ys (ys [R_max, H],
     gates fp32 [T, top_k] or None, y [T, H])."""
-    T, H = y.shape
-    _want("y", y, _BF16, T, H, rows=True)
-    _want("ys", ys, _BF16, None, H, rows=True)
-    _want("inv_perm", inv_perm, _I32, T * top_k)
-    if gates is not None:
-        _want("gates", gates, _F32, T, top_k)
-    _on_device("e4b_unpermute", stream, (ys, inv_perm, gates, y), _addr(ys), _ld(ys), ys.shape[0], H,
-               _addr(inv_perm), _addr(gates), T, top_k, _addr(y), _ld(y))
+    T, H = _matrix("y", y)
+    R, dev = _matrix("ys", ys)[0], y.get_device()
+    _call("e4b_unpermute", dev, stream, *_rows("ys", ys, R, H, dev), R, H,
+          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev),
+          None if gates is None else _vec("gates", gates, _F32, (T, top_k), dev), T, top_k,
+          *_rows("y", y, T, H, dev))
 
 
 def e4b_unpermute_backward(dy, ys, inv_perm, gates, dys, dgates, *, top_k, stream=None):
     """dys[inv_perm[s]] = gates[s] dy[t] and dgates[s] = <dy[t], ys[inv_perm[s]]>;
     dys or dgates may be None, and ys where dgates is."""
-    T, H = dy.shape
-    _want("dy", dy, _BF16, T, H, rows=True)
-    _want("inv_perm", inv_perm, _I32, T * top_k)
-    if gates is not None:
-        _want("gates", gates, _F32, T, top_k)
-    rows = [t for t in (ys, dys) if t is not None]
-    if not rows or (dgates is not None and ys is None):
+    T, H = _matrix("dy", dy)
+    dev = dy.get_device()
+    if (ys is None and dys is None) or (ys is None and dgates is not None) or (dys is None and dgates is None):
         raise ValueError("ys is needed for dgates, dys or dgates for a result")
-    for name, t in (("ys", ys), ("dys", dys)):
-        if t is not None:
-            _want(name, t, _BF16, rows[0].shape[0], H, rows=True)
-    if dgates is not None:
-        _want("dgates", dgates, _F32, T, top_k)
-    _on_device("e4b_unpermute_backward", stream, (dy, ys, inv_perm, gates, dys, dgates), _addr(dy), _ld(dy),
-               _addr(ys), 0 if ys is None else _ld(ys), rows[0].shape[0], H, _addr(inv_perm), _addr(gates), T, top_k,
-               _addr(dys), 0 if dys is None else _ld(dys), _addr(dgates))
+    R = _matrix("ys", dys if ys is None else ys)[0]
+    _call("e4b_unpermute_backward", dev, stream, *_rows("dy", dy, T, H, dev),
+          *((None, 0) if ys is None else _rows("ys", ys, R, H, dev)), R, H,
+          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev),
+          None if gates is None else _vec("gates", gates, _F32, (T, top_k), dev), T, top_k,
+          *((None, 0) if dys is None else _rows("dys", dys, R, H, dev)),
+          None if dgates is None else _vec("dgates", dgates, _F32, (T, top_k), dev))
 
 
 def _glu_args(gu, offsets, layout, act, alpha, limit):
-    R, I2 = gu.shape
+    R, I2 = _matrix("gu", gu)
+    dev = gu.get_device()
     if I2 % 2:
         raise ValueError("gu: rows of 2I values")
-    _want("gu", gu, _BF16, R, I2, rows=True)
     a = GluArgs(0, LAYOUT[layout], ACT[act], alpha, limit, I2 // 2, R)
     if offsets is not None:
-        _want("offsets", offsets, _I64, None)
-        a.E, a.offsets = offsets.numel() - 1, _addr(offsets)
-    a.gu, a.ld_gu = _addr(gu), _ld(gu)
-    return a, R, I2 // 2
+        a.E = offsets.numel() - 1
+        a.offsets = _vec("offsets", offsets, _I64, (a.E + 1,), dev)
+    a.gu, a.ld_gu = _rows("gu", gu, R, I2, dev)
+    return a, R, I2 // 2, dev
 
 
 def e4b_glu(gu, h, *, offsets=None, layout="halves", act="swiglu", alpha=1.702, limit=7.0, stream=None):
     """h = the gated activation of stored gate_up rows (gu [R_max, 2I], h
     [R_max, I]); with offsets only of the rows p < offsets[E]."""
-    a, R, I = _glu_args(gu, offsets, layout, act, alpha, limit)
-    _want("h", h, _BF16, R, I, rows=True)
-    a.h, a.ld_h = _addr(h), _ld(h)
-    _on_device("e4b_glu", stream, (gu, h, offsets), ctypes.byref(a))
+    a, R, I, dev = _glu_args(gu, offsets, layout, act, alpha, limit)
+    a.h, a.ld_h = _rows("h", h, R, I, dev)
+    _call("e4b_glu", dev, stream, a)
 
 
 def e4b_glu_backward(dh, gu, dgu, *, h=None, offsets=None, layout="halves", act="swiglu", alpha=1.702, limit=7.0,
                      stream=None):
     """dgu = the gradient of e4b_glu for dh; dgu may be gu. With h the
     activation itself is written again too."""
-    a, R, I = _glu_args(gu, offsets, layout, act, alpha, limit)
-    _want("dh", dh, _BF16, R, I, rows=True)
-    _want("dgu", dgu, _BF16, R, 2 * I, rows=True)
-    a.dh, a.ld_dh, a.dgu, a.ld_dgu = _addr(dh), _ld(dh), _addr(dgu), _ld(dgu)
+    a, R, I, dev = _glu_args(gu, offsets, layout, act, alpha, limit)
+    a.dh, a.ld_dh = _rows("dh", dh, R, I, dev)
+    a.dgu, a.ld_dgu = _rows("dgu", dgu, R, 2 * I, dev)
     if h is not None:
-        _want("h", h, _BF16, R, I, rows=True)
-        a.h, a.ld_h = _addr(h), _ld(h)
-    _on_device("e4b_glu_backward", stream, (dh, gu, dgu, h, offsets), ctypes.byref(a))
+        a.h, a.ld_h = _rows("h", h, R, I, dev)
+    _call("e4b_glu_backward", dev, stream, a)
 
 
 def e4b_lora_workspace_size(G, r, N, K, R_max, backward=False) -> int:
@@ -571,24 +576,17 @@ def e4b_lora_workspace_size(G, r, N, K, R_max, backward=False) -> int:
     return n.value
 
 
-def _lora_args(a, b, offsets, scale, row, R_max, rows):
-    """The part of the arguments both directions share. rows: the tensors
-    [rows, *] that positions point into."""
+def _lora_args(a, b, offsets, scale, row, n, dev):
+    """The arguments both directions share; n: rows that positions point into."""
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a: expected [G, r, K], b: expected [G, N, r]")
     G, r, K = a.shape
-    N = b.shape[1] if b.dim() == 3 else -1
-    _want("a", a, _BF16, G, r, K)
-    _want("b", b, _BF16, G, N, r)
-    _want("offsets", offsets, _I64, G + 1)
-    if scale is not None:
-        _want("scale", scale, _F32, G)
-    n = rows[0][1].shape[0]
-    for name, t, width in rows:
-        _want(name, t, _BF16, n, width(N, K), rows=True)
-    if row is not None:
-        _want("row", row, _I32, R_max)
-    elif n != R_max:
-        raise ValueError(f"{rows[0][0]}: expected {R_max} rows, got {n}")
-    return LoraArgs(G, r, N, K, R_max, _addr(a), _addr(b), _addr(scale), _addr(offsets), _addr(row), n)
+    N = b.shape[1]
+    R_max = n if row is None else row.numel()
+    return LoraArgs(G, r, N, K, R_max, _vec("a", a, _BF16, (G, r, K), dev), _vec("b", b, _BF16, (G, N, r), dev),
+                    None if scale is None else _vec("scale", scale, _F32, (G,), dev),
+                    _vec("offsets", offsets, _I64, (G + 1,), dev),
+                    None if row is None else _vec("row", row, _I32, (R_max,), dev), n)
 
 
 def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=None, row=None, layout="halves",
@@ -597,25 +595,20 @@ def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=N
     positions p of every group g, i = row[p] (p without row); of s, y and h
     those that are given are written. a [G, r, K], b [G, N, r], x [*, K], base
     and y [*, N], h [*, N/2], s fp32 [R_max, r], scale fp32 [G], row [R_max]."""
-    R_max = row.numel() if row is not None else x.shape[0]
-    rows = [("x", x, lambda N, K: K)]
-    rows += [(n, t, lambda N, K: N) for n, t in (("base", base), ("y", y)) if t is not None]
-    rows += [("h", h, lambda N, K: N // 2)] if h is not None else []
-    p = _lora_args(a, b, offsets, scale, row, R_max, rows)
-    p.x, p.ld_x = _addr(x), _ld(x)
+    n, dev = _matrix("x", x)[0], x.get_device()
+    p = _lora_args(a, b, offsets, scale, row, n, dev)
+    p.x, p.ld_x = _rows("x", x, n, p.K, dev)
     if s is not None:
-        _want("s", s, _F32, R_max, p.r)
-        p.s = _addr(s)
+        p.s = _vec("s", s, _F32, (p.R_max, p.r), dev)
     if base is not None:
-        p.base, p.ld_base = _addr(base), _ld(base)
+        p.base, p.ld_base = _rows("base", base, n, p.N, dev)
     if y is not None:
-        p.y, p.ld_y = _addr(y), _ld(y)
+        p.y, p.ld_y = _rows("y", y, n, p.N, dev)
     if h is not None:
-        p.h, p.ld_h = _addr(h), _ld(h)
+        p.h, p.ld_h = _rows("h", h, n, p.N // 2, dev)
         p.gate_up_layout, p.activation, p.glu_alpha, p.glu_limit = LAYOUT[layout], ACT[act], alpha, limit
-    _want("ws", ws, torch.uint8, None)
-    _on_device("e4b_lora", stream, (x, a, b, offsets, ws, base, y, h, s, scale, row), ctypes.byref(p), _addr(ws),
-               ws.numel(), 0)
+    nb = ws.numel()
+    _call("e4b_lora", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb, 0)
 
 
 def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=None, db=None, accumulate=False,
@@ -625,29 +618,24 @@ def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=
     scale[g] B_g^T dy[i]; those of dx, da (fp32 [G, r, K]) and db (fp32 [G, N, r])
     that are given. accumulate: da and db are added to. x may be None without
     da, s without db."""
-    R_max = row.numel() if row is not None else dy.shape[0]
-    rows = [("dy", dy, lambda N, K: N)]
-    rows += [(n, t, lambda N, K: K) for n, t in (("x", x), ("dx", dx), ("dx_base", dx_base)) if t is not None]
-    p = _lora_args(a, b, offsets, scale, row, R_max, rows)
-    p.dy, p.ld_dy = _addr(dy), _ld(dy)
+    n, dev = _matrix("dy", dy)[0], dy.get_device()
+    p = _lora_args(a, b, offsets, scale, row, n, dev)
+    p.dy, p.ld_dy = _rows("dy", dy, n, p.N, dev)
     if x is not None:
-        p.x, p.ld_x = _addr(x), _ld(x)
+        p.x, p.ld_x = _rows("x", x, n, p.K, dev)
     if s is not None:
-        _want("s", s, _F32, R_max, p.r)
-        p.s = _addr(s)
+        p.s = _vec("s", s, _F32, (p.R_max, p.r), dev)
     if dx is not None:
-        p.dx, p.ld_dx = _addr(dx), _ld(dx)
+        p.dx, p.ld_dx = _rows("dx", dx, n, p.K, dev)
     if dx_base is not None:
-        p.dx_base, p.ld_dx_base = _addr(dx_base), _ld(dx_base)
+        p.dx_base, p.ld_dx_base = _rows("dx_base", dx_base, n, p.K, dev)
     if da is not None:
-        _want("da", da, _F32, p.G, p.r, p.K)
-        p.da = _addr(da)
+        p.da = _vec("da", da, _F32, (p.G, p.r, p.K), dev)
     if db is not None:
-        _want("db", db, _F32, p.G, p.N, p.r)
-        p.db = _addr(db)
-    _want("ws", ws, torch.uint8, None)
-    _on_device("e4b_lora_backward", stream, (dy, a, b, offsets, ws, x, s, dx, dx_base, da, db, scale, row),
-               ctypes.byref(p), _addr(ws), ws.numel(), FLAG_ACCUMULATE if accumulate else 0)
+        p.db = _vec("db", db, _F32, (p.G, p.N, p.r), dev)
+    nb = ws.numel()
+    _call("e4b_lora_backward", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb,
+          FLAG_ACCUMULATE if accumulate else 0)
 
 
 # ---------------------------------------------------------------- the layer
