@@ -1,6 +1,7 @@
 // Host-side launchers of the adapter path's kernels, used by the C-ABI layer
 // (api.cu): token rows by expert and back (csrc/rows.cu), the gated activation
-// on stored rows (csrc/glu.cu) and the grouped low-rank adapters (csrc/lora.cu).
+// on stored rows (csrc/glu.cu) and the grouped low-rank adapters (csrc/lora.cu,
+// csrc/lora_tc.cu).
 #pragma once
 
 #include <cstddef>
@@ -35,8 +36,8 @@ cudaError_t launch_glu(const e4b_glu_args& a, bool backward, cudaStream_t st, in
 // Largest adapter rank of the kernels.
 constexpr int kLoraMaxRank = 64;
 size_t lora_workspace_bytes(int64_t G, int r, int64_t N, int64_t K, int64_t R_max, bool backward, int sms);
-cudaError_t launch_lora(const e4b_lora_args& a, void* ws, cudaStream_t st, int sms, int* launches);
-cudaError_t launch_lora_backward(const e4b_lora_args& a, bool accumulate, void* ws, cudaStream_t st, int sms,
+cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaStream_t st, int sms, int* launches);
+cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flags, cudaStream_t st, int sms,
                                  int* launches);
 
 }  // namespace e4b

@@ -569,7 +569,7 @@ static e4b_status check_lora(const e4b_lora_args* a, void* ws, size_t ws_bytes, 
 }
 
 e4b_status e4b_lora(const e4b_lora_args* a, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
-  if (!a || flags) return E4B_ERR_INVALID_ARG;
+  if (!a || (flags & ~E4B_FLAG_TEST_TIMEOUT)) return E4B_ERR_INVALID_ARG;
   e4b_status st = check_lora_sizes(a->G, a->r, a->N, a->K, a->R_max);
   if (st != E4B_OK) return st;
   if (a->h) {
@@ -586,13 +586,13 @@ e4b_status e4b_lora(const e4b_lora_args* a, void* ws, size_t ws_bytes, uint32_t 
   if (a->h && (st = check_rows(a->h, a->ld_h, a->N / 2)) != E4B_OK) return st;
   if (a->y && a->y == a->base && a->ld_y != a->ld_base) return E4B_ERR_INVALID_ARG;
   int launches = 0;
-  st = cuda_status(launch_lora(*a, ws, static_cast<cudaStream_t>(stream), sm_count(), &launches));
+  st = cuda_status(launch_lora(*a, ws, flags, static_cast<cudaStream_t>(stream), sm_count(), &launches));
   g_last_launches = launches;
   return st;
 }
 
 e4b_status e4b_lora_backward(const e4b_lora_args* a, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
-  if (!a || (flags & ~E4B_FLAG_ACCUMULATE)) return E4B_ERR_INVALID_ARG;
+  if (!a || (flags & ~(E4B_FLAG_ACCUMULATE | E4B_FLAG_TEST_TIMEOUT))) return E4B_ERR_INVALID_ARG;
   e4b_status st = check_lora_sizes(a->G, a->r, a->N, a->K, a->R_max);
   if (st != E4B_OK) return st;
   g_last_launches = 0;
@@ -607,8 +607,7 @@ e4b_status e4b_lora_backward(const e4b_lora_args* a, void* ws, size_t ws_bytes, 
     if (a->dx && a->dx == a->dx_base && a->ld_dx != a->ld_dx_base) return E4B_ERR_INVALID_ARG;
   }
   int launches = 0;
-  st = cuda_status(launch_lora_backward(*a, (flags & E4B_FLAG_ACCUMULATE) != 0, ws, static_cast<cudaStream_t>(stream),
-                                        sm_count(), &launches));
+  st = cuda_status(launch_lora_backward(*a, ws, flags, static_cast<cudaStream_t>(stream), sm_count(), &launches));
   g_last_launches = launches;
   return st;
 }

@@ -1,0 +1,797 @@
+// The adapters' contractions on the 5th-generation tensor cores: one pass over
+// a buffer of bf16 rows z_i, in groups of positions p (i = row ? row[p] : p),
+// for either or both of
+//   out[p] = w_g W_g z_i            over a row's C columns (s = A x, t = w B^T dy)
+//   grad_g = sum_p w_g v[p] z_i^T   over a group's positions (dB from dy, dA from x)
+// Both contract the same tile of 128 positions x 128 columns, the first along
+// its columns and the second along its rows, so a backward pass reads dy once
+// for two results. With r <= 64 the pass moves 2 bytes for every 2 r (out) or
+// 6 r (grad) FLOP and is bound by HBM; the tensor cores read the tile from
+// shared memory in both directions (K-major and MN-major descriptors of the
+// same 128B-swizzled boxes), so no thread touches it.
+//
+// Numbers: z and W enter as they are (bf16), sums are fp32 in TMEM. The fp32
+// values v enter as three bf16 terms hi + mid + lo (24 bits of mantissa), which
+// makes the fp32 gradients as exact as fp32 products: two terms left a relative
+// error of 2^-17 a product. The terms lie side by side as columns of one B
+// operand (N = 3 * rank) up to rank 32, and are added when TMEM is read: three
+// MMAs into one accumulator would read the tile from shared memory three times.
+//
+// One persistent CTA per SM. The work is the list of (column block, row tile)
+// in that order, cut into equal runs for the CTAs, so that the groups' sizes do
+// not unbalance it; a CTA accumulates a group's gradient in TMEM over the
+// consecutive row tiles of its run, and writes it to its place when it took all
+// the group's tiles, else (the first and last of its run) to a part that
+// finish_kernel sums in CTA order: results depend on the sizes alone.
+//   warp 0       TMA: W's box, and the tile's where its rows lie together and
+//                are all of the group
+//   warp 1       TMEM and the single-thread MMA issue
+//   warps 2-5    v's terms of each row tile, in the operand's layout
+//   warps 6-9    TMEM to out and grad
+//   warps 10-13  the other tiles, by cp.async into the same swizzled boxes: mapped
+//                rows, and with grad the last ones of a group, where a row of no
+//                position reads as zeros so that no other group's values meet
+//                these (four-row TMA gathers of such tiles took 45 ns each, three
+//                times as long as whole boxes: 180 against 62 us for 65536 rows
+//                of 2048)
+// Every wait is bounded; one that gives up records E4B_ERR_DEVICE_TIMEOUT,
+// stops all roles, drains the copies and MMAs in flight, frees TMEM and returns.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "lora_tc.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace e4b {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 448;
+constexpr int kLoadWarp = 10, kLoadWarps = 4;
+constexpr int kTile = 128;                       // positions, and columns, of a tile
+constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
+constexpr uint32_t kZBytes = 2 * kBox;           // a tile
+constexpr int kMaxStages = 6;
+constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
+constexpr uint32_t kSmemLimit = 232448;
+
+struct Pass {
+  int64_t C, R_max, rows, ld_z;
+  const uint16_t* z;
+  const int64_t* offsets;
+  const int32_t* row;
+  const float* scale;
+  float* out;
+  const float* v;
+  float* grad;
+  float* grad_part;
+  int32_t* status;
+  int G, r, rp;        // rp: the rank's operand width, 16, 32 or 64
+  int blocks, chunks;  // column blocks; column tiles of a block
+  int stages, vbufs;
+  uint32_t limit;
+  uint8_t w_t, scale_out, scale_v, grad_t, accumulate, merged;
+};
+
+// Shared memory, from a 1024-byte boundary: stages of (tile, W's box), the
+// buffers of v's terms, then barriers and scalars.
+struct Layout {
+  uint32_t stage, terms, misc, total;
+};
+__host__ __device__ inline Layout layout_of(const Pass& p, bool out, bool grad) {
+  Layout l;
+  l.stage = kZBytes + (out ? 2 * kTile * p.rp : 0);
+  l.terms = l.stage * p.stages;
+  l.misc = l.terms + (grad ? p.vbufs * 6 * kTile * p.rp : 0);
+  l.total = l.misc + 1024 + 1024;  // barriers and scalars, alignment
+  return l;
+}
+
+__host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, int64_t R_max, int64_t& beg, int64_t& end) {
+  beg = offsets[g];
+  end = offsets[g + 1];
+  beg = beg < 0 ? 0 : beg > R_max ? R_max : beg;  // no position outside [0, R_max) is ever formed
+  end = end < 0 ? 0 : end > R_max ? R_max : end;
+  return end > beg ? (end - beg + kTile - 1) / kTile : 0;
+}
+
+// First item of CTA b's run out of W items over n CTAs, and the CTA of an item.
+__host__ __device__ inline int64_t run_start(int64_t W, int64_t n, int64_t b) { return b * W / n; }
+__host__ __device__ inline int64_t run_of(int64_t W, int64_t n, int64_t w) { return ((w + 1) * n - 1) / W; }
+
+// A position in the list of (column block, row tile), row tiles in group order.
+struct Walk {
+  const int64_t* offsets;
+  int64_t R_max, beg, end, tiles;
+  int64_t tile;  // within the group
+  int G, g, cb;
+
+  E4B_DEV void enter(int group) {
+    g = group;
+    tiles = group_tiles(offsets, g, R_max, beg, end);
+  }
+  E4B_DEV void next() {
+    if (++tile < tiles) return;
+    tile = 0;
+    do {
+      if (g + 1 == G) ++cb;
+      enter(g + 1 == G ? 0 : g + 1);
+    } while (tiles == 0);  // some group has rows
+  }
+  E4B_DEV bool first() const { return tile == 0; }
+  E4B_DEV bool last() const { return tile + 1 == tiles; }
+  E4B_DEV int64_t row0() const { return beg + tile * kTile; }
+  E4B_DEV int n() const { return int(end - row0() < kTile ? end - row0() : kTile); }
+};
+
+// Descriptor of an operand without swizzle: core matrices of 8 x 16 bytes, lbo
+// bytes apart along K and sbo along M or N.
+E4B_DEV uint64_t plain_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46);
+}
+// Descriptor of an MN-major operand one swizzle span (32, 64 or 128 bytes)
+// wide: 8 K-rows of a span after one another.
+E4B_DEV uint64_t span_desc(uint32_t saddr, uint32_t span) {
+  const uint64_t layout = span == 128 ? 2 : span == 64 ? 4 : 6;
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t((8 * span) >> 4) << 32) |
+         (uint64_t(1) << 46) | (layout << 61);
+}
+
+E4B_DEV float finite_rest(float v, float h) { return fabsf(h) < INFINITY ? v - h : 0.f; }
+
+// Eight values as three bf16 terms; infinities and NaN have only the first.
+E4B_DEV void split3(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
+  uint32_t t[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      t[k][i] = pack_bf16x2(a, b);
+      a = finite_rest(a, __uint_as_float(t[k][i] << 16));
+      b = finite_rest(b, __uint_as_float(t[k][i] & 0xFFFF0000u));
+    }
+  }
+  hi = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+  mid = make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
+  lo = make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
+}
+
+template <bool OUT, bool GRAD>
+__global__ void __launch_bounds__(kThreads, 1)
+contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ Pass p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Layout lay = layout_of(p, OUT, GRAD);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.misc);
+  uint64_t* loaded = full + kMaxStages;
+  uint64_t* empty = loaded + kMaxStages;
+  uint64_t* t_full = empty + kMaxStages;
+  uint64_t* t_empty = t_full + 2;
+  uint64_t* v_full = t_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* g_full = v_empty + 2;
+  uint64_t* g_empty = g_full + 1;  // [kMaxChunks]
+  int64_t* s_sum = reinterpret_cast<int64_t*>(g_empty + kMaxChunks);  // [kThreads / 32 + 1]
+  int64_t* s_start = s_sum + kThreads / 32 + 1;                       // group, tile
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_start + 2);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // the row tiles of all groups, and where this CTA's run begins
+  const int per = (p.G + kThreads - 1) / kThreads;
+  const int g_lo = min(tid * per, p.G), g_hi = min(g_lo + per, p.G);
+  int64_t beg, end, mine = 0;
+  for (int g = g_lo; g < g_hi; ++g) mine += group_tiles(p.offsets, g, p.R_max, beg, end);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, T = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    T += s_sum[w];
+  }
+  const int64_t W = T * p.blocks;
+  const int64_t n_run = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
+  if (int64_t(blockIdx.x) >= n_run) return;  // uniform; also where no group has rows
+  const int64_t w0 = run_start(W, n_run, blockIdx.x), w1 = run_start(W, n_run, int64_t(blockIdx.x) + 1);
+  const int64_t rt0 = w0 % T;
+  if (rt0 >= before && rt0 < before + mine) {
+    int64_t left = rt0 - before;
+    for (int g = g_lo; g < g_hi; ++g) {
+      const int64_t t = group_tiles(p.offsets, g, p.R_max, beg, end);
+      if (left < t) {
+        s_start[0] = g;
+        s_start[1] = left;
+        break;
+      }
+      left -= t;
+    }
+  }
+  const bool loads = GRAD || p.row;  // some tiles may be the loaders'
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&loaded[s], kLoadWarps);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&t_full[b], 1);
+      mbar_init(&t_empty[b], 128);
+      mbar_init(&v_full[b], 128);
+      mbar_init(&v_empty[b], 1);
+    }
+    mbar_init(g_full, 1);
+    if (GRAD)
+      for (int c = 0; c < p.chunks; ++c) mbar_init(&g_empty[c], 128);
+    *s_abort = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  const int64_t count = w1 - w0;
+  const int all_chunks = int((p.C + kTile - 1) / kTile);
+  const int rp = p.rp, gw = p.merged ? 3 * rp : rp;  // TMEM columns of a tile's gradient
+  const uint32_t d_grad = tmem + (OUT ? 2 * rp : 0);
+  Walk wk;
+  wk.offsets = p.offsets;
+  wk.R_max = p.R_max;
+  wk.G = p.G;
+  wk.cb = int(w0 / T);
+  wk.enter(int(s_start[0]));
+  wk.tile = s_start[1];
+  auto chunks_of = [&](int cb) { return min(p.chunks, all_chunks - cb * p.chunks); };
+  auto give_up = [&]() {
+    *s_abort = 1;
+    record_status(p.status, E4B_ERR_DEVICE_TIMEOUT);
+  };
+
+  // whole: TMA brings the tile. Without grad the rows past a group's end only
+  // make results that are not written.
+  auto whole = [&]() { return !p.row && (!GRAD || wk.n() == kTile); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      int64_t i = 0;
+      bool aborted = false;
+      for (int64_t k = 0; k < count && !aborted; ++k) {
+        const bool box = whole();
+        const int32_t row0 = int32_t(wk.row0());
+        const uint32_t bytes = (box ? kZBytes : 0) + (OUT ? 2 * kTile * rp : 0);
+        const int nc = chunks_of(wk.cb);
+        for (int c = 0; c < nc; ++c, ++i) {
+          const int s = int(i % p.stages);
+          if (!mbar_wait_bounded(&empty[s], (uint32_t(i / p.stages) & 1u) ^ 1u, p.limit, s_abort)) {
+            give_up();
+            aborted = true;
+            break;
+          }
+          uint8_t* dst = smem + s * lay.stage;
+          const int32_t x = (wk.cb * p.chunks + c) * kTile;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          if (box) {
+            tma_load_2d(dst, &tm_tile, &full[s], x, row0);
+            tma_load_2d(dst + kBox, &tm_tile, &full[s], x + 64, row0);
+          }
+          if (OUT) {
+            if (p.w_t) {
+              tma_load_3d(dst + kZBytes, &tm_w, &full[s], 0, x, wk.g);
+            } else {
+              tma_load_3d(dst + kZBytes, &tm_w, &full[s], x, 0, wk.g);
+              tma_load_3d(dst + kZBytes + 128 * rp, &tm_w, &full[s], x + 64, 0, wk.g);
+            }
+          }
+        }
+        if (k + 1 < count) wk.next();
+      }
+      // every copy issued has to land before the CTA can exit
+      for (int64_t q = i > p.stages ? i - p.stages : 0; q < i; ++q)
+        mbar_wait_bounded(&full[q % p.stages], uint32_t(q / p.stages) & 1u, kWaitPolls, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t id_out = idesc_bf16_f32(kTile, rp) | (p.w_t ? 1u << 16 : 0u);
+      const uint32_t id_grad = idesc_bf16_f32(kTile, gw) | (1u << 15) | (1u << 16);  // both MN-major
+      const uint32_t vk = uint32_t(3 * rp / 8) * 128;  // bytes of 8 positions of v's terms
+      int64_t i = 0;
+      uint32_t g_phase = 0;
+      uint64_t* last_bar = nullptr;
+      uint32_t last_ph = 0;
+      bool aborted = false;
+      bool fresh = true;  // first row tile of a gradient
+      for (int64_t k = 0; k < count && !aborted; ++k) {
+        const int tb = int(k & 1), vb = p.vbufs == 2 ? tb : 0;
+        const int64_t vuse = p.vbufs == 2 ? k >> 1 : k;
+        if ((OUT && !mbar_wait_bounded(&t_empty[tb], (uint32_t(k >> 1) & 1u) ^ 1u, p.limit, s_abort)) ||
+            (GRAD && !mbar_wait_bounded(&v_full[vb], uint32_t(vuse) & 1u, p.limit, s_abort))) {
+          give_up();
+          break;
+        }
+        const int steps = (wk.n() + 15) / 16;
+        const int nc = chunks_of(wk.cb);
+        const uint32_t terms = smem_u32(smem + lay.terms + vb * 6 * kTile * rp);
+        for (int c = 0; c < nc; ++c, ++i) {
+          const int s = int(i % p.stages);
+          if (!mbar_wait_bounded(&full[s], uint32_t(i / p.stages) & 1u, p.limit, s_abort) ||
+              (loads && !mbar_wait_bounded(&loaded[s], uint32_t(i / p.stages) & 1u, p.limit, s_abort)) ||
+              (GRAD && fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
+            give_up();
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t z = smem_u32(smem + s * lay.stage), w = z + kZBytes;
+          if (OUT) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t half = kk >> 2, in = kk & 3;
+              const uint64_t wd = p.w_t ? span_desc(w + uint32_t(kk) * 32 * rp, 2 * rp)
+                                        : sw128_kmajor_desc(w + half * 128 * rp + in * 32);
+              mma_bf16_ss(tmem + tb * rp, sw128_kmajor_desc(z + half * kBox + in * 32), wd, id_out, (c | kk) ? 1u : 0u);
+            }
+          }
+          if (GRAD) {
+            if (fresh) g_phase ^= 1u << c;
+            const uint32_t d = d_grad + uint32_t(c * gw);
+            for (int kk = 0; kk < steps; ++kk) {
+              const uint64_t zd = sw128_mnmajor_desc(z + kk * 2048, kBox, 1024);
+              const uint32_t vd = terms + uint32_t(kk) * 2 * vk;
+              if (p.merged) {
+                mma_bf16_ss(d, zd, plain_desc(vd, vk, 128), id_grad, !fresh || kk ? 1u : 0u);
+              } else {  // the small terms first
+                for (int t = 2; t >= 0; --t)
+                  mma_bf16_ss(d, zd, plain_desc(vd + uint32_t(t) * rp * 16, vk, 128), id_grad,
+                              !fresh || kk || t < 2 ? 1u : 0u);
+              }
+            }
+          }
+          mma_commit(&empty[s]);
+          last_bar = &empty[s];
+          last_ph = uint32_t(i / p.stages) & 1u;
+        }
+        if (aborted) break;
+        if (OUT) mma_commit(&t_full[tb]);
+        if (GRAD) {
+          mma_commit(&v_empty[vb]);
+          fresh = wk.last();
+          if (fresh || k + 1 == count) mma_commit(g_full);
+        }
+        if (k + 1 < count) wk.next();
+      }
+      // the MMAs issued so far have to finish before TMEM is freed
+      if (*s_abort && last_bar) mbar_wait_bounded(last_bar, last_ph, kWaitPolls, nullptr);
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------- v's terms, a thread a position
+    if constexpr (GRAD) {
+      const int m = tid - 64;
+      uint8_t* mine_at = smem + lay.terms + (m >> 3) * (3 * rp / 8) * 128 + (m & 7) * 16;
+      for (int64_t k = 0; k < count; ++k) {
+        const int vb = p.vbufs == 2 ? int(k & 1) : 0;
+        const int64_t vuse = p.vbufs == 2 ? k >> 1 : k;
+        const int64_t pos = wk.row0() + m;
+        bool in = m < wk.n();
+        if (in && p.row) {
+          const int32_t at = __ldg(p.row + pos);
+          in = at >= 0 && at < p.rows;
+        }
+        const float w = p.scale_v && p.scale ? __ldg(p.scale + wk.g) : 1.f;
+        float4 x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          x[j] = in && 4 * j < p.r ? __ldg(reinterpret_cast<const float4*>(p.v + pos * p.r) + j)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!mbar_wait_bounded(&v_empty[vb], (uint32_t(vuse) & 1u) ^ 1u, p.limit, s_abort)) {
+          give_up();
+          break;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (8 * j >= rp) break;
+          const float f[8] = {w * x[2 * j].x, w * x[2 * j].y, w * x[2 * j].z, w * x[2 * j].w,
+                              w * x[2 * j + 1].x, w * x[2 * j + 1].y, w * x[2 * j + 1].z, w * x[2 * j + 1].w};
+          uint4 hi, mid, lo;
+          split3(f, hi, mid, lo);
+          uint8_t* dst = mine_at + vb * 6 * kTile * rp + j * 128;
+          *reinterpret_cast<uint4*>(dst) = hi;
+          *reinterpret_cast<uint4*>(dst + rp * 16) = mid;
+          *reinterpret_cast<uint4*>(dst + rp * 32) = lo;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&v_full[vb]);
+        if (k + 1 < count) wk.next();
+      }
+    }
+  } else if (warp >= kLoadWarp) {
+    // --------------------------------------- rows that TMA does not bring
+    // A warp copies 32 rows of the tile, two at a time, and tells of a stage
+    // when the copies of the stages after it are under way too.
+    if (loads) {
+      const int m0 = (warp - kLoadWarp) * 32;
+      const int piece = lane & 15;  // 16 bytes of a row's 256
+      int64_t i = 0, told = 0;
+      bool aborted = false;
+      auto tell = [&](int64_t upto) {  // the copies of stages before upto have landed
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (; told < upto; ++told)
+          if (lane == 0) mbar_arrive(&loaded[told % p.stages]);
+      };
+      for (int64_t k = 0; k < count && !aborted; ++k) {
+        const bool box = whole();
+        const int n = wk.n();
+        const int rows = GRAD ? (n + 15) / 16 * 16 : n;  // that the MMAs read, or whose results count
+        int32_t at = -1;  // row m0 + lane
+        if (!box && m0 + lane < n) {
+          at = p.row ? __ldg(p.row + wk.row0() + m0 + lane) : int32_t(wk.row0()) + m0 + lane;
+          if (at >= p.rows) at = -1;
+        }
+        const int nc = chunks_of(wk.cb);
+        for (int c = 0; c < nc; ++c, ++i) {
+          const int s = int(i % p.stages);
+          if (!mbar_wait_bounded(&empty[s], (uint32_t(i / p.stages) & 1u) ^ 1u, p.limit, s_abort)) {
+            give_up();
+            aborted = true;
+            break;
+          }
+          if (!box) {
+            const int64_t x = int64_t(wk.cb * p.chunks + c) * kTile + 8 * piece;
+            uint8_t* dst = smem + s * lay.stage + (piece >> 3) * kBox;
+#pragma unroll 4
+            for (int r2 = 0; r2 < 32; r2 += 2) {
+              const int r = r2 + (lane >> 4);
+              const int32_t row = __shfl_sync(0xffffffffu, at, r);
+              if (m0 + r >= rows) continue;
+              const bool on = row >= 0 && x < p.C;
+              const uint16_t* src = p.z + (on ? int64_t(row) * p.ld_z + x : 0);
+              cp_async_16(dst + (m0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4), src, on ? 16 : 0);
+            }
+          }
+          cp_async_commit();
+          if (p.stages > 3) {
+            if (i >= 3) {
+              cp_async_wait<3>();
+              tell(i - 2);
+            }
+          } else if (i >= 2) {
+            cp_async_wait<2>();
+            tell(i - 1);
+          }
+        }
+        if (k + 1 < count) wk.next();
+      }
+      cp_async_wait_all();
+      tell(i);
+    }
+  } else {
+    // ---------------------------------------------------- results from TMEM
+    const int q = warp & 3;  // the TMEM lanes this warp may read
+    const int m = q * 32 + lane;
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    int64_t seg0 = 0;  // first item of the gradient's row tiles in this run
+    uint32_t segs = 0;
+    bool whole_start = wk.first();
+    for (int64_t k = 0; k < count; ++k) {
+      const int tb = int(k & 1);
+      if constexpr (OUT) {
+        if (!mbar_wait_bounded(&t_full[tb], uint32_t(k >> 1) & 1u, p.limit, s_abort)) {
+          give_up();
+          break;
+        }
+        tc_fence_after();
+        const bool in = m < wk.n();
+        const float w = p.scale_out && p.scale ? __ldg(p.scale + wk.g) : 1.f;
+        float* dst = p.out + (int64_t(wk.cb) * p.R_max + wk.row0() + m) * p.r;
+        for (int j0 = 0; j0 < rp; j0 += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + lanes + tb * rp + j0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            if (in && j0 + j < p.r)
+              *reinterpret_cast<float4*>(dst + j0 + j) =
+                  make_float4(w * __uint_as_float(v[j]), w * __uint_as_float(v[j + 1]), w * __uint_as_float(v[j + 2]),
+                              w * __uint_as_float(v[j + 3]));
+        }
+        tc_fence_before();
+        mbar_arrive(&t_empty[tb]);
+      }
+      if constexpr (GRAD) {
+        const bool done = wk.last();
+        if (done || k + 1 == count) {
+          if (!mbar_wait_bounded(g_full, segs & 1u, p.limit, s_abort)) {
+            give_up();
+            break;
+          }
+          tc_fence_after();
+          const bool direct = whole_start && done;
+          const int64_t block = int64_t(p.chunks) * kTile;  // columns of a part
+          const int64_t col0 = direct ? wk.cb * block : 0, width = direct ? p.C : block;
+          float* dst = direct ? p.grad + int64_t(wk.g) * p.C * p.r
+                              : p.grad_part + (2 * int64_t(blockIdx.x) + (seg0 == 0 ? 0 : 1)) * block * p.r;
+          const bool add = direct && p.accumulate;
+          const int nc = chunks_of(wk.cb);
+          for (int c = 0; c < nc; ++c) {
+            const int64_t n = int64_t(c) * kTile + m;
+            const bool in = wk.cb * block + n < p.C;
+            for (int j0 = 0; j0 < rp; j0 += 16) {
+              float f[16];
+              uint32_t v[16];
+              const uint32_t at = d_grad + lanes + uint32_t(c * gw + j0);
+              tmem_ld_32x32b_x16(at, v);
+              if (p.merged) {
+                uint32_t v1[16], v2[16];
+                tmem_ld_32x32b_x16(at + rp, v1);
+                tmem_ld_32x32b_x16(at + 2 * rp, v2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  f[j] = (__uint_as_float(v2[j]) + __uint_as_float(v1[j])) + __uint_as_float(v[j]);
+              } else {
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+              }
+              if (j0 + 16 >= rp) {
+                tc_fence_before();
+                mbar_arrive(&g_empty[c]);
+              }
+              if (!in) continue;
+              if (p.grad_t) {
+                float4* at4 = reinterpret_cast<float4*>(dst + (col0 + n) * p.r + j0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (j0 + 4 * j >= p.r) break;
+                  float4 o = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                  if (add) {
+                    const float4 w = at4[j];
+                    o = make_float4(w.x + o.x, w.y + o.y, w.z + o.z, w.w + o.w);
+                  }
+                  at4[j] = o;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  if (j0 + j >= p.r) break;
+                  float* at1 = dst + int64_t(j0 + j) * width + col0 + n;
+                  *at1 = add ? *at1 + f[j] : f[j];
+                }
+              }
+            }
+          }
+          ++segs;
+          seg0 = k + 1;
+          whole_start = true;  // the next one begins with its group
+        }
+      }
+      if (k + 1 < count) wk.next();
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The gradients that several CTAs share (the parts' sum, in CTA order) and
+// those of groups without rows (zero). CTA (x, y): piece x of a column block's
+// values of group y.
+struct Finish {
+  Pass p;
+  int64_t grid;  // CTAs of the pass
+};
+constexpr int kFinishPieces = 4;
+
+E4B_DEV void finish_one(const Finish& f, int piece, int g) {
+  const Pass& p = f.p;
+  const int cb = piece / kFinishPieces, sub = piece % kFinishPieces;
+  __shared__ int64_t s_before[8], s_all[8];
+  const int tid = threadIdx.x;
+  int64_t beg, end, before = 0, all = 0;
+  for (int k = tid; k < p.G; k += 256) {
+    const int64_t t = group_tiles(p.offsets, k, p.R_max, beg, end);
+    all += t;
+    if (k < g) before += t;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+  }
+  __syncthreads();
+  if ((tid & 31) == 0) {
+    s_before[tid >> 5] = before;
+    s_all[tid >> 5] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+  for (int k = 0; k < 8; ++k) {
+    before += s_before[k];
+    all += s_all[k];
+  }
+  const int64_t tiles = group_tiles(p.offsets, g, p.R_max, beg, end);
+  const int64_t W = all * p.blocks, n_run = W < f.grid ? W : f.grid;
+  int64_t b0 = 0, b1 = -1;
+  int slot0 = 0;  // b0's first or last part; the others end or lie within the group: their first
+  if (tiles) {
+    const int64_t w0 = cb * all + before;
+    b0 = run_of(W, n_run, w0);
+    slot0 = run_start(W, n_run, b0) < w0;
+    b1 = run_of(W, n_run, w0 + tiles - 1);
+    if (b0 == b1) return;  // that CTA wrote it
+  } else if (p.accumulate) {
+    return;
+  }
+  const int64_t block = int64_t(p.chunks) * kTile, c0 = cb * block;
+  const int cols = int(min(block, p.C - c0));
+  // values that lie together: the block's columns by r, or r rows of its columns
+  const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
+  float* dst = p.grad + int64_t(g) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
+  for (int i = sub * 256 + tid; i < lines * len4; i += 256 * kFinishPieces) {
+    const int line = i / len4, at = (i - line * len4) * 4;
+    float4* out = reinterpret_cast<float4*>(dst + line * p.C + at);
+    float4 s = p.accumulate ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* src = p.grad_part + line * block + at;
+    for (int64_t b = b0; b <= b1; ++b) {
+      const float4 v = *reinterpret_cast<const float4*>(src + (2 * b + (b == b0 ? slot0 : 0)) * block * p.r);
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+    *out = s;
+  }
+}
+
+__global__ void __launch_bounds__(256)
+finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (int(blockIdx.x) < a.p.blocks * kFinishPieces)
+    finish_one(a, blockIdx.x, blockIdx.y);
+  else
+    finish_one(b, blockIdx.x - a.p.blocks * kFinishPieces, blockIdx.y);
+}
+
+// ---------------------------------------------------------------- the plan
+struct Plan {
+  int rp, merged, chunks, blocks, vbufs, stages;
+};
+
+// Column tiles of a block: as many as TMEM holds the gradients of (a part of
+// `out`, or of a group cut between CTAs, costs 4 r bytes a row or column), but
+// so few that the list has about eight items for each SM.
+Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
+  Plan q;
+  q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  q.merged = q.rp <= 32;
+  const int gw = q.merged ? 3 * q.rp : q.rp;
+  int most = grad ? (512 - (out ? 2 * q.rp : 0)) / gw : 64;
+  if (grad && most > kMaxChunks) most = kMaxChunks;
+  const int64_t all = (C + kTile - 1) / kTile;
+  const int64_t groups = G < R_max ? G : R_max;
+  const int64_t tiles = R_max / kTile + (groups + 1) / 2;
+  int64_t want = all * tiles / (int64_t(sms) * (grad ? 8 : 2));
+  if (want < 1) want = 1;
+  if (want > most) want = most;
+  q.blocks = int((all + want - 1) / want);
+  q.chunks = int((all + q.blocks - 1) / q.blocks);
+  q.blocks = int((all + q.chunks - 1) / q.chunks);
+  q.vbufs = q.rp <= 32 ? 2 : 1;
+  const int64_t terms = grad ? int64_t(q.vbufs) * 6 * kTile * q.rp : 0;
+  const int64_t stage = kZBytes + (out ? 2 * kTile * q.rp : 0);
+  q.stages = int((int64_t(kSmemLimit) - 2048 - terms) / stage);
+  if (q.stages > kMaxStages) q.stages = kMaxStages;
+  return q;
+}
+
+Pass pass_of(const ContractArgs& a, const Plan& q) {
+  Pass p{};
+  p.C = a.C;
+  p.R_max = a.R_max;
+  p.rows = a.row ? a.rows : a.R_max;
+  p.ld_z = a.ld_z;
+  p.z = a.z;
+  p.offsets = a.offsets;
+  p.row = a.row;
+  p.scale = a.scale;
+  p.out = a.out;
+  p.v = a.v;
+  p.grad = a.grad;
+  p.grad_part = a.grad_part;
+  p.status = a.status;
+  p.G = a.G;
+  p.r = a.r;
+  p.rp = q.rp;
+  p.blocks = q.blocks;
+  p.chunks = q.chunks;
+  p.stages = q.stages;
+  p.vbufs = q.vbufs;
+  p.limit = a.no_wait ? 0u : kWaitPolls;
+  p.w_t = a.w_t;
+  p.scale_out = a.scale_out;
+  p.scale_v = a.scale_v;
+  p.grad_t = a.grad_t;
+  p.accumulate = a.accumulate;
+  p.merged = q.merged;
+  return p;
+}
+
+template <bool OUT, bool GRAD>
+cudaError_t launch(const CUtensorMap& tile, const CUtensorMap& w, const Pass& p, cudaStream_t st, int sms) {
+  auto kernel = contract_kernel<OUT, GRAD>;
+  const uint32_t smem = layout_of(p, OUT, GRAD).total;
+  // set on every call: the attribute belongs to the device that is current
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (err != cudaSuccess) return err;
+  return launch_dependent(kernel, dim3(sms), dim3(kThreads), smem, st, tile, w, p);
+}
+
+}  // namespace
+
+int contract_blocks(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
+  return plan_of(G, r, C, R_max, out, grad, sms).blocks;
+}
+
+size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int sms) {
+  return size_t(2) * sms * plan_of(G, r, C, R_max, out, true, sms).chunks * kTile * r * 4;
+}
+
+cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
+  const Plan q = plan_of(a.G, a.r, a.C, a.R_max, a.out != nullptr, a.grad != nullptr, sms);
+  const Pass p = pass_of(a, q);
+  CUtensorMap tile, w;
+  bool ok = encode_2d(&tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
+                      64, kTile, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (a.out) {
+    // a group's matrix is a plane of its own, so that a box past its edge reads zeros
+    const CUtensorMapSwizzle span = q.rp == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                    : q.rp == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
+    ok = ok && (a.w_t ? encode_planes(&w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.r, a.C, a.G, 2, q.rp, kTile, span)
+                      : encode_planes(&w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.C, a.r, a.G, 2, 64, q.rp,
+                                      CU_TENSOR_MAP_SWIZZLE_128B));
+  } else {
+    w = tile;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if (!a.grad) return launch<true, false>(tile, w, p, st, sms);
+  if (!a.out) return launch<false, true>(tile, w, p, st, sms);
+  return launch<true, true>(tile, w, p, st, sms);
+}
+
+cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
+  Finish f[2] = {};
+  int blocks = 0, i = 0, G = 0;
+  for (const ContractArgs* c : {a, b}) {
+    if (!c) continue;
+    f[i].p = pass_of(*c, plan_of(c->G, c->r, c->C, c->R_max, c->out != nullptr, true, sms));
+    f[i].grid = sms;
+    blocks += f[i].p.blocks * kFinishPieces;
+    G = c->G;
+    ++i;
+  }
+  return launch_dependent(finish_kernel, dim3(unsigned(blocks), unsigned(G)), dim3(256), 0, st, f[0], f[1]);
+}
+
+}  // namespace e4b

@@ -125,6 +125,7 @@ class LoraArgs(ctypes.Structure):
         ("glu_limit", ctypes.c_float), ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
         ("dx_base", ctypes.c_void_p), ("ld_dx_base", ctypes.c_int64), ("dx", ctypes.c_void_p),
         ("ld_dx", ctypes.c_int64), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -590,11 +591,12 @@ def _lora_args(a, b, offsets, scale, row, n, dev):
 
 
 def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=None, row=None, layout="halves",
-             act="swiglu", alpha=1.702, limit=7.0, stream=None):
+             act="swiglu", alpha=1.702, limit=7.0, status=None, flags=0, stream=None):
     """s[p] = A_g x[i], y[i] = base[i] + scale[g] B_g s[p] and h = act(y) for the
     positions p of every group g, i = row[p] (p without row); of s, y and h
     those that are given are written. a [G, r, K], b [G, N, r], x [*, K], base
-    and y [*, N], h [*, N/2], s fp32 [R_max, r], scale fp32 [G], row [R_max]."""
+    and y [*, N], h [*, N/2], s fp32 [R_max, r], scale fp32 [G], row [R_max],
+    status int32 [1], zeroed by the caller."""
     n, dev = _matrix("x", x)[0], x.get_device()
     p = _lora_args(a, b, offsets, scale, row, n, dev)
     p.x, p.ld_x = _rows("x", x, n, p.K, dev)
@@ -607,12 +609,14 @@ def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=N
     if h is not None:
         p.h, p.ld_h = _rows("h", h, n, p.N // 2, dev)
         p.gate_up_layout, p.activation, p.glu_alpha, p.glu_limit = LAYOUT[layout], ACT[act], alpha, limit
+    if status is not None:
+        p.status = _vec("status", status, _I32, (1,), dev)
     nb = ws.numel()
-    _call("e4b_lora", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb, 0)
+    _call("e4b_lora", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb, flags)
 
 
 def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=None, db=None, accumulate=False,
-                      scale=None, row=None, stream=None):
+                      scale=None, row=None, status=None, flags=0, stream=None):
     """The gradients of e4b_lora for dy [*, N]: dx[i] = dx_base[i] + A_g^T t[p],
     da[g] = sum_p t[p] x[i]^T and db[g] = scale[g] sum_p dy[i] s[p]^T with t[p] =
     scale[g] B_g^T dy[i]; those of dx, da (fp32 [G, r, K]) and db (fp32 [G, N, r])
@@ -633,9 +637,11 @@ def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=
         p.da = _vec("da", da, _F32, (p.G, p.r, p.K), dev)
     if db is not None:
         p.db = _vec("db", db, _F32, (p.G, p.N, p.r), dev)
+    if status is not None:
+        p.status = _vec("status", status, _I32, (1,), dev)
     nb = ws.numel()
     _call("e4b_lora_backward", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb,
-          FLAG_ACCUMULATE if accumulate else 0)
+          flags | (FLAG_ACCUMULATE if accumulate else 0))
 
 
 # ---------------------------------------------------------------- the layer

@@ -580,14 +580,18 @@ e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
  * rows of two positions must differ; an entry outside [0, rows) leaves its
  * position out (s[p] = 0, no row written, nothing added to the gradients).
  * Rows of no position are left as they were.
- * fp32 accumulation; s and t enter the second product as two bf16 terms (16
- * bits of mantissa); every reduction runs in a fixed order, so repeated calls
- * give the same bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
+ * fp32 accumulation; s and t enter a product with a bf16 result as two bf16
+ * terms (16 bits of mantissa), one with an fp32 result (da, db) as three (24
+ * bits); every reduction runs in a fixed order, so repeated calls give the same
+ * bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
  * with zeros; an adapter of a higher rank is the sum of two, the second with
  * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max <= 2^30;
  * all pointers but offsets, row and scale 16-byte aligned. ws: device scratch of
  * e4b_lora_workspace_size bytes (16-byte aligned), for one call at a time.
- * Launches: 2 forward, up to 4 backward.
+ * flags: E4B_FLAG_ACCUMULATE (backward), E4B_FLAG_TEST_TIMEOUT. A wait on the GPU
+ * that gives up records E4B_ERR_DEVICE_TIMEOUT in *status (the caller zeroes it)
+ * and leaves results unwritten.
+ * Launches: 2 forward, up to 5 backward.
  */
 #define E4B_FLAG_ACCUMULATE 0x100u /* e4b_lora_backward: add to da and db */
 
@@ -620,6 +624,7 @@ typedef struct {
   int64_t ld_dx;
   float* da;
   float* db;
+  int32_t* status; /* optional device int32 that records E4B_ERR_DEVICE_TIMEOUT */
 } e4b_lora_args;
 
 /* Host: workspace bytes of e4b_lora (backward == 0) or e4b_lora_backward. */
