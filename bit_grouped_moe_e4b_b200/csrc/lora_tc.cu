@@ -23,17 +23,15 @@
 // consecutive row tiles of its run, and writes it to its place when it took all
 // the group's tiles, else (the first and last of its run) to a part that
 // finish_kernel sums in CTA order: results depend on the sizes alone.
-//   warp 0       TMA: W's box, and the tile's where its rows lie together and
-//                are all of the group
+//   warp 0       TMA: W's box, and the tile's where its rows lie together (in
+//                boxes of 32 rows at a group's end)
 //   warp 1       TMEM and the single-thread MMA issue
 //   warps 2-5    v's terms of each row tile, in the operand's layout
 //   warps 6-9    TMEM to out and grad
-//   warps 10-13  the other tiles, by cp.async into the same swizzled boxes: mapped
-//                rows, and with grad the last ones of a group, where a row of no
-//                position reads as zeros so that no other group's values meet
-//                these (four-row TMA gathers of such tiles took 45 ns each, three
-//                times as long as whole boxes: 180 against 62 us for 65536 rows
-//                of 2048)
+//   warps 10-13  mapped rows, by cp.async into the same swizzled boxes (four-row
+//                TMA gathers took 45 ns each: three times as long as whole boxes),
+//                and zeros in place of the rows behind a group's end that a
+//                gradient's MMAs read, so that no other group's values meet these
 // Every wait is bounded; one that gives up records E4B_ERR_DEVICE_TIMEOUT,
 // stops all roles, drains the copies and MMAs in flight, frees TMEM and returns.
 #include <cuda.h>
@@ -52,6 +50,7 @@ constexpr int kThreads = 448;
 constexpr int kLoadWarp = 10, kLoadWarps = 4;
 constexpr int kTile = 128;                       // positions, and columns, of a tile
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
+constexpr int kEdge = 32;                        // rows of the boxes at a group's end
 constexpr uint32_t kZBytes = 2 * kBox;           // a tile
 constexpr int kMaxStages = 6;
 constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
@@ -126,18 +125,43 @@ struct Walk {
   E4B_DEV int n() const { return int(end - row0() < kTile ? end - row0() : kTile); }
 };
 
-// Descriptor of an operand without swizzle: core matrices of 8 x 16 bytes, lbo
-// bytes apart along K and sbo along M or N.
+// Shared-memory descriptors, built once: a step adds its bytes / 16 to the low
+// word (the address field cannot overflow into its neighbour below 256 KB).
+// Without swizzle: core matrices of 8 x 16 bytes, lbo bytes apart along K and
+// sbo along M or N.
 E4B_DEV uint64_t plain_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46);
 }
-// Descriptor of an MN-major operand one swizzle span (32, 64 or 128 bytes)
-// wide: 8 K-rows of a span after one another.
+// MN-major, one swizzle span (32, 64 or 128 bytes) wide: 8 K-rows of a span
+// after one another.
 E4B_DEV uint64_t span_desc(uint32_t saddr, uint32_t span) {
   const uint64_t layout = span == 128 ? 2 : span == 64 ? 4 : 6;
   return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t((8 * span) >> 4) << 32) |
          (uint64_t(1) << 46) | (layout << 61);
+}
+E4B_DEV uint64_t step_desc(uint64_t d, uint32_t bytes) {
+  return (d & 0xFFFFFFFF00000000ull) | uint32_t(uint32_t(d) + (bytes >> 4));
+}
+
+// A slot of a ring and the parity of its use, without a division.
+struct Ring {
+  int n, slot = 0;
+  uint32_t parity = 0;
+  E4B_DEV explicit Ring(int slots) : n(slots) {}
+  E4B_DEV void next() {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// A warp's wait: one lane polls.
+E4B_DEV bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit, const volatile int* abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, limit, abort);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 E4B_DEV float finite_rest(float v, float h) { return fabsf(h) < INFINITY ? v - h : 0.f; }
@@ -162,8 +186,8 @@ E4B_DEV void split3(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
 
 template <bool OUT, bool GRAD>
 __global__ void __launch_bounds__(kThreads, 1)
-contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_constant__ CUtensorMap tm_w,
-                const __grid_constant__ Pass p) {
+contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_constant__ CUtensorMap tm_edge,
+                const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ Pass p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Layout lay = layout_of(p, OUT, GRAD);
@@ -220,7 +244,6 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       left -= t;
     }
   }
-  const bool loads = GRAD || p.row;  // some tiles may be the loaders'
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -265,40 +288,50 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     record_status(p.status, E4B_ERR_DEVICE_TIMEOUT);
   };
 
-  // whole: TMA brings the tile. Without grad the rows past a group's end only
-  // make results that are not written.
-  auto whole = [&]() { return !p.row && (!GRAD || wk.n() == kTile); };
+  // The loaders have a part in every stage or in none: a parity wait must never
+  // be two uses of its barrier away, so no role may skip stages that another
+  // walks. Without grad the rows past a group's end only make results that are
+  // not written.
+  const bool loaders = GRAD || p.row;
+  // rows of the tile that the MMAs read, or whose results count
+  auto rows_read = [&]() { return GRAD ? (wk.n() + 15) / 16 * 16 : wk.n(); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
     if (lane == 0) {
+      Ring st(p.stages);
       int64_t i = 0;
       bool aborted = false;
       for (int64_t k = 0; k < count && !aborted; ++k) {
-        const bool box = whole();
         const int32_t row0 = int32_t(wk.row0());
-        const uint32_t bytes = (box ? kZBytes : 0) + (OUT ? 2 * kTile * rp : 0);
+        const int edges = p.row ? 0 : (rows_read() + kEdge - 1) / kEdge;
+        const uint32_t bytes = edges * (kEdge * 256) + (OUT ? 2 * kTile * rp : 0);
         const int nc = chunks_of(wk.cb);
-        for (int c = 0; c < nc; ++c, ++i) {
-          const int s = int(i % p.stages);
-          if (!mbar_wait_bounded(&empty[s], (uint32_t(i / p.stages) & 1u) ^ 1u, p.limit, s_abort)) {
+        int32_t x = wk.cb * p.chunks * kTile;
+        for (int c = 0; c < nc; ++c, ++i, x += kTile, st.next()) {
+          if (!mbar_wait_bounded(&empty[st.slot], st.parity ^ 1u, p.limit, s_abort)) {
             give_up();
             aborted = true;
             break;
           }
-          uint8_t* dst = smem + s * lay.stage;
-          const int32_t x = (wk.cb * p.chunks + c) * kTile;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          if (box) {
-            tma_load_2d(dst, &tm_tile, &full[s], x, row0);
-            tma_load_2d(dst + kBox, &tm_tile, &full[s], x + 64, row0);
+          uint64_t* bar = &full[st.slot];
+          uint8_t* dst = smem + st.slot * lay.stage;
+          mbar_arrive_expect_tx(bar, bytes);
+          if (edges == kTile / kEdge) {
+            tma_load_2d(dst, &tm_tile, bar, x, row0);
+            tma_load_2d(dst + kBox, &tm_tile, bar, x + 64, row0);
+          } else {
+            for (int e = 0; e < edges; ++e) {
+              tma_load_2d(dst + e * kEdge * 128, &tm_edge, bar, x, row0 + e * kEdge);
+              tma_load_2d(dst + e * kEdge * 128 + kBox, &tm_edge, bar, x + 64, row0 + e * kEdge);
+            }
           }
           if (OUT) {
             if (p.w_t) {
-              tma_load_3d(dst + kZBytes, &tm_w, &full[s], 0, x, wk.g);
+              tma_load_3d(dst + kZBytes, &tm_w, bar, 0, x, wk.g);
             } else {
-              tma_load_3d(dst + kZBytes, &tm_w, &full[s], x, 0, wk.g);
-              tma_load_3d(dst + kZBytes + 128 * rp, &tm_w, &full[s], x + 64, 0, wk.g);
+              tma_load_3d(dst + kZBytes, &tm_w, bar, x, 0, wk.g);
+              tma_load_3d(dst + kZBytes + 128 * rp, &tm_w, bar, x + 64, 0, wk.g);
             }
           }
         }
@@ -314,69 +347,82 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       const uint32_t id_out = idesc_bf16_f32(kTile, rp) | (p.w_t ? 1u << 16 : 0u);
       const uint32_t id_grad = idesc_bf16_f32(kTile, gw) | (1u << 15) | (1u << 16);  // both MN-major
       const uint32_t vk = uint32_t(3 * rp / 8) * 128;  // bytes of 8 positions of v's terms
-      int64_t i = 0;
+      // W's steps along its 128 columns: 16 of them, 64 of them
+      const uint32_t w_step = p.w_t ? 32 * rp : 32, w_half = 128 * rp;
+      const uint32_t z0 = smem_u32(smem);
+      const uint64_t zk = sw128_kmajor_desc(z0), zm = sw128_mnmajor_desc(z0, kBox, 1024);
+      const uint64_t wd0 = p.w_t ? span_desc(z0 + kZBytes, 2 * rp) : sw128_kmajor_desc(z0 + kZBytes);
+      const uint64_t vd0 = plain_desc(z0 + lay.terms, vk, 128);
+      Ring st(p.stages), vr(p.vbufs), tr(2);
       uint32_t g_phase = 0;
       uint64_t* last_bar = nullptr;
       uint32_t last_ph = 0;
       bool aborted = false;
       bool fresh = true;  // first row tile of a gradient
       for (int64_t k = 0; k < count && !aborted; ++k) {
-        const int tb = int(k & 1), vb = p.vbufs == 2 ? tb : 0;
-        const int64_t vuse = p.vbufs == 2 ? k >> 1 : k;
-        if ((OUT && !mbar_wait_bounded(&t_empty[tb], (uint32_t(k >> 1) & 1u) ^ 1u, p.limit, s_abort)) ||
-            (GRAD && !mbar_wait_bounded(&v_full[vb], uint32_t(vuse) & 1u, p.limit, s_abort))) {
+        if ((OUT && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort)) ||
+            (GRAD && !mbar_wait_bounded(&v_full[vr.slot], vr.parity, p.limit, s_abort))) {
           give_up();
           break;
         }
         const int steps = (wk.n() + 15) / 16;
         const int nc = chunks_of(wk.cb);
-        const uint32_t terms = smem_u32(smem + lay.terms + vb * 6 * kTile * rp);
-        for (int c = 0; c < nc; ++c, ++i) {
-          const int s = int(i % p.stages);
-          if (!mbar_wait_bounded(&full[s], uint32_t(i / p.stages) & 1u, p.limit, s_abort) ||
-              (loads && !mbar_wait_bounded(&loaded[s], uint32_t(i / p.stages) & 1u, p.limit, s_abort)) ||
+        const uint64_t vd = step_desc(vd0, vr.slot * 6 * kTile * rp);
+        const uint32_t d_out = tmem + tr.slot * rp;
+        uint32_t d = d_grad;
+        for (int c = 0; c < nc; ++c, d += gw, st.next()) {
+          if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
+              (loaders && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
               (GRAD && fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
             give_up();
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t z = smem_u32(smem + s * lay.stage), w = z + kZBytes;
+          const uint32_t at = st.slot * lay.stage;
           if (OUT) {
+            const uint64_t zd = step_desc(zk, at), wd = step_desc(wd0, at);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t half = kk >> 2, in = kk & 3;
-              const uint64_t wd = p.w_t ? span_desc(w + uint32_t(kk) * 32 * rp, 2 * rp)
-                                        : sw128_kmajor_desc(w + half * 128 * rp + in * 32);
-              mma_bf16_ss(tmem + tb * rp, sw128_kmajor_desc(z + half * kBox + in * 32), wd, id_out, (c | kk) ? 1u : 0u);
-            }
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ss(d_out, step_desc(zd, (kk >> 2) * kBox + (kk & 3) * 32),
+                          step_desc(wd, uint32_t(kk >> 2) * w_half + uint32_t(kk & 3) * w_step), id_out, (c | kk) ? 1u : 0u);
           }
           if (GRAD) {
             if (fresh) g_phase ^= 1u << c;
-            const uint32_t d = d_grad + uint32_t(c * gw);
-            for (int kk = 0; kk < steps; ++kk) {
-              const uint64_t zd = sw128_mnmajor_desc(z + kk * 2048, kBox, 1024);
-              const uint32_t vd = terms + uint32_t(kk) * 2 * vk;
-              if (p.merged) {
-                mma_bf16_ss(d, zd, plain_desc(vd, vk, 128), id_grad, !fresh || kk ? 1u : 0u);
-              } else {  // the small terms first
-                for (int t = 2; t >= 0; --t)
-                  mma_bf16_ss(d, zd, plain_desc(vd + uint32_t(t) * rp * 16, vk, 128), id_grad,
-                              !fresh || kk || t < 2 ? 1u : 0u);
+            const uint64_t zd = step_desc(zm, at);
+            if (p.merged) {
+              uint64_t vs = vd;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                if (kk < steps) mma_bf16_ss(d, step_desc(zd, kk * 2048), vs, id_grad, !fresh || kk ? 1u : 0u);
+                vs = step_desc(vs, 2 * vk);
+              }
+            } else {  // the small terms first
+              uint64_t vs = vd;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                if (kk < steps) {
+                  mma_bf16_ss(d, step_desc(zd, kk * 2048), step_desc(vs, 32 * rp), id_grad, !fresh || kk ? 1u : 0u);
+                  mma_bf16_ss(d, step_desc(zd, kk * 2048), step_desc(vs, 16 * rp), id_grad, 1u);
+                  mma_bf16_ss(d, step_desc(zd, kk * 2048), vs, id_grad, 1u);
+                }
+                vs = step_desc(vs, 2 * vk);
               }
             }
           }
-          mma_commit(&empty[s]);
-          last_bar = &empty[s];
-          last_ph = uint32_t(i / p.stages) & 1u;
+          mma_commit(&empty[st.slot]);
+          last_bar = &empty[st.slot];
+          last_ph = st.parity;
         }
         if (aborted) break;
-        if (OUT) mma_commit(&t_full[tb]);
+        if (OUT) mma_commit(&t_full[tr.slot]);
         if (GRAD) {
-          mma_commit(&v_empty[vb]);
+          mma_commit(&v_empty[vr.slot]);
           fresh = wk.last();
           if (fresh || k + 1 == count) mma_commit(g_full);
         }
+        tr.next();
+        vr.next();
         if (k + 1 < count) wk.next();
       }
       // the MMAs issued so far have to finish before TMEM is freed
@@ -387,9 +433,8 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     if constexpr (GRAD) {
       const int m = tid - 64;
       uint8_t* mine_at = smem + lay.terms + (m >> 3) * (3 * rp / 8) * 128 + (m & 7) * 16;
+      Ring vr(p.vbufs);
       for (int64_t k = 0; k < count; ++k) {
-        const int vb = p.vbufs == 2 ? int(k & 1) : 0;
-        const int64_t vuse = p.vbufs == 2 ? k >> 1 : k;
         const int64_t pos = wk.row0() + m;
         bool in = m < wk.n();
         if (in && p.row) {
@@ -402,7 +447,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         for (int j = 0; j < 16; ++j)
           x[j] = in && 4 * j < p.r ? __ldg(reinterpret_cast<const float4*>(p.v + pos * p.r) + j)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!mbar_wait_bounded(&v_empty[vb], (uint32_t(vuse) & 1u) ^ 1u, p.limit, s_abort)) {
+        if (!warp_wait(&v_empty[vr.slot], vr.parity ^ 1u, p.limit, s_abort)) {
           give_up();
           break;
         }
@@ -413,76 +458,102 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
                               w * x[2 * j + 1].x, w * x[2 * j + 1].y, w * x[2 * j + 1].z, w * x[2 * j + 1].w};
           uint4 hi, mid, lo;
           split3(f, hi, mid, lo);
-          uint8_t* dst = mine_at + vb * 6 * kTile * rp + j * 128;
+          uint8_t* dst = mine_at + vr.slot * 6 * kTile * rp + j * 128;
           *reinterpret_cast<uint4*>(dst) = hi;
           *reinterpret_cast<uint4*>(dst + rp * 16) = mid;
           *reinterpret_cast<uint4*>(dst + rp * 32) = lo;
         }
         fence_proxy_async_smem();
-        mbar_arrive(&v_full[vb]);
+        mbar_arrive(&v_full[vr.slot]);
+        vr.next();
         if (k + 1 < count) wk.next();
       }
     }
   } else if (warp >= kLoadWarp) {
-    // --------------------------------------- rows that TMA does not bring
-    // A warp copies 32 rows of the tile, two at a time, and tells of a stage
-    // when the copies of the stages after it are under way too.
-    if (loads) {
-      const int m0 = (warp - kLoadWarp) * 32;
-      const int piece = lane & 15;  // 16 bytes of a row's 256
-      int64_t i = 0, told = 0;
+    // ---------------------------- rows that TMA does not bring, or not alone
+    const int w4 = warp - kLoadWarp;
+    if (p.row) {
+      // A warp copies 32 rows of the tile, two at a time, and tells of a stage
+      // when the copies of the stages after it are under way too.
+      const int m0 = w4 * 32, hi = lane >> 4, piece = lane & 15;  // 16 bytes of a row's 256
+      Ring st(p.stages), told(p.stages);
+      int pending = 0;
       bool aborted = false;
-      auto tell = [&](int64_t upto) {  // the copies of stages before upto have landed
+      auto tell = [&]() {  // the copies of the oldest stage have landed
         fence_proxy_async_smem();
         __syncwarp();
-        for (; told < upto; ++told)
-          if (lane == 0) mbar_arrive(&loaded[told % p.stages]);
+        if (lane == 0) mbar_arrive(&loaded[told.slot]);
+        told.next();
+        --pending;
       };
       for (int64_t k = 0; k < count && !aborted; ++k) {
-        const bool box = whole();
-        const int n = wk.n();
-        const int rows = GRAD ? (n + 15) / 16 * 16 : n;  // that the MMAs read, or whose results count
+        const int n = wk.n(), rows = rows_read();
         int32_t at = -1;  // row m0 + lane
-        if (!box && m0 + lane < n) {
-          at = p.row ? __ldg(p.row + wk.row0() + m0 + lane) : int32_t(wk.row0()) + m0 + lane;
+        if (m0 + lane < n) {
+          at = __ldg(p.row + wk.row0() + m0 + lane);
           if (at >= p.rows) at = -1;
         }
+        const uint16_t* src[16];  // of rows m0 + 2 u + hi; those of no position read as zeros
+        uint32_t on = 0;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int32_t row = __shfl_sync(0xffffffffu, at, 2 * u + hi);
+          if (row >= 0) on |= 1u << u;
+          src[u] = p.z + (row >= 0 ? int64_t(row) * p.ld_z + 8 * piece : 0);
+        }
         const int nc = chunks_of(wk.cb);
-        for (int c = 0; c < nc; ++c, ++i) {
-          const int s = int(i % p.stages);
-          if (!mbar_wait_bounded(&empty[s], (uint32_t(i / p.stages) & 1u) ^ 1u, p.limit, s_abort)) {
+        int64_t x = int64_t(wk.cb) * p.chunks * kTile;
+        for (int c = 0; c < nc; ++c, x += kTile, st.next()) {
+          if (!warp_wait(&empty[st.slot], st.parity ^ 1u, p.limit, s_abort)) {
             give_up();
             aborted = true;
             break;
           }
-          if (!box) {
-            const int64_t x = int64_t(wk.cb * p.chunks + c) * kTile + 8 * piece;
-            uint8_t* dst = smem + s * lay.stage + (piece >> 3) * kBox;
-#pragma unroll 4
-            for (int r2 = 0; r2 < 32; r2 += 2) {
-              const int r = r2 + (lane >> 4);
-              const int32_t row = __shfl_sync(0xffffffffu, at, r);
-              if (m0 + r >= rows) continue;
-              const bool on = row >= 0 && x < p.C;
-              const uint16_t* src = p.z + (on ? int64_t(row) * p.ld_z + x : 0);
-              cp_async_16(dst + (m0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4), src, on ? 16 : 0);
-            }
+          const bool in = x + 8 * piece < p.C;
+          uint8_t* dst = smem + st.slot * lay.stage + (piece >> 3) * kBox + (m0 + hi) * 128;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            if (m0 + 2 * u + hi >= rows) continue;
+            const bool yes = in && (on >> u & 1u);
+            cp_async_16(dst + u * 256 + (((piece & 7) ^ ((2 * u + hi) & 7)) << 4), yes ? src[u] + x : p.z, yes ? 16 : 0);
           }
           cp_async_commit();
+          ++pending;
           if (p.stages > 3) {
-            if (i >= 3) {
+            if (pending > 3) {
               cp_async_wait<3>();
-              tell(i - 2);
+              tell();
             }
-          } else if (i >= 2) {
+          } else if (pending > 2) {
             cp_async_wait<2>();
-            tell(i - 1);
+            tell();
           }
         }
         if (k + 1 < count) wk.next();
       }
       cp_async_wait_all();
-      tell(i);
+      while (pending) tell();
+    } else if (GRAD) {
+      // zeros behind a group's last row, up to the MMA's next step of 16
+      Ring st(p.stages);
+      bool aborted = false;
+      for (int64_t k = 0; k < count && !aborted; ++k) {
+        const int n = wk.n(), rows = rows_read(), nc = chunks_of(wk.cb);
+        for (int c = 0; c < nc; ++c, st.next()) {
+          if (!warp_wait(&full[st.slot], st.parity, p.limit, s_abort)) {
+            give_up();
+            aborted = true;
+            break;
+          }
+          uint8_t* z = smem + st.slot * lay.stage + (lane >> 3 & 1) * kBox + (lane & 7) * 16;
+          for (int m = n + 2 * w4 + (lane >> 4); m < rows; m += 2 * kLoadWarps)
+            *reinterpret_cast<uint4*>(z + m * 128) = make_uint4(0, 0, 0, 0);
+          if (n < rows) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&loaded[st.slot]);
+        }
+        if (k + 1 < count) wk.next();
+      }
     }
   } else {
     // ---------------------------------------------------- results from TMEM
@@ -492,10 +563,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     int64_t seg0 = 0;  // first item of the gradient's row tiles in this run
     uint32_t segs = 0;
     bool whole_start = wk.first();
-    for (int64_t k = 0; k < count; ++k) {
-      const int tb = int(k & 1);
+    Ring tr(2);
+    for (int64_t k = 0; k < count; ++k, tr.next()) {
       if constexpr (OUT) {
-        if (!mbar_wait_bounded(&t_full[tb], uint32_t(k >> 1) & 1u, p.limit, s_abort)) {
+        if (!warp_wait(&t_full[tr.slot], tr.parity, p.limit, s_abort)) {
           give_up();
           break;
         }
@@ -505,7 +576,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         float* dst = p.out + (int64_t(wk.cb) * p.R_max + wk.row0() + m) * p.r;
         for (int j0 = 0; j0 < rp; j0 += 16) {
           uint32_t v[16];
-          tmem_ld_32x32b_x16(tmem + lanes + tb * rp + j0, v);
+          tmem_ld_32x32b_x16(tmem + lanes + tr.slot * rp + j0, v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; j += 4)
@@ -515,12 +586,12 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
                               w * __uint_as_float(v[j + 3]));
         }
         tc_fence_before();
-        mbar_arrive(&t_empty[tb]);
+        mbar_arrive(&t_empty[tr.slot]);
       }
       if constexpr (GRAD) {
         const bool done = wk.last();
         if (done || k + 1 == count) {
-          if (!mbar_wait_bounded(g_full, segs & 1u, p.limit, s_abort)) {
+          if (!warp_wait(g_full, segs & 1u, p.limit, s_abort)) {
             give_up();
             break;
           }
@@ -678,9 +749,11 @@ struct Plan {
   int rp, merged, chunks, blocks, vbufs, stages;
 };
 
-// Column tiles of a block: as many as TMEM holds the gradients of (a part of
-// `out`, or of a group cut between CTAs, costs 4 r bytes a row or column), but
-// so few that the list has about eight items for each SM.
+// Column tiles of a block: at most those whose gradients TMEM holds, and of
+// these the number with the least time by this estimate, in units of one tile's
+// 32 KB from HBM: the longest run's items (half a unit each besides their
+// tiles), the last gradients' way out of TMEM, the parts of `out` written and
+// read again. Row tiles are an estimate: groups may end anywhere in one.
 Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
   Plan q;
   q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
@@ -690,12 +763,19 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   if (grad && most > kMaxChunks) most = kMaxChunks;
   const int64_t all = (C + kTile - 1) / kTile;
   const int64_t groups = G < R_max ? G : R_max;
-  const int64_t tiles = R_max / kTile + (groups + 1) / 2;
-  int64_t want = all * tiles / (int64_t(sms) * (grad ? 8 : 2));
-  if (want < 1) want = 1;
-  if (want > most) want = most;
-  q.blocks = int((all + want - 1) / want);
-  q.chunks = int((all + q.blocks - 1) / q.blocks);
+  const int64_t tiles = R_max / kTile + (groups + 1) / 2;  // > 0, if there are rows
+  double best = 0;
+  q.chunks = 0;
+  for (int64_t c = 1; c <= most && c <= all; ++c) {
+    const int64_t blocks = (all + c - 1) / c, items = blocks * tiles;
+    double t = double((items + sms - 1) / sms) * (double(c) + 0.5);
+    if (grad) t += 0.5 * double(c);
+    if (out && blocks > 1) t += double(items) * r / (32.0 * sms);
+    if (!q.chunks || t <= best) {
+      best = t;
+      q.chunks = int(c);
+    }
+  }
   q.blocks = int((all + q.chunks - 1) / q.chunks);
   q.vbufs = q.rp <= 32 ? 2 : 1;
   const int64_t terms = grad ? int64_t(q.vbufs) * 6 * kTile * q.rp : 0;
@@ -738,13 +818,13 @@ Pass pass_of(const ContractArgs& a, const Plan& q) {
 }
 
 template <bool OUT, bool GRAD>
-cudaError_t launch(const CUtensorMap& tile, const CUtensorMap& w, const Pass& p, cudaStream_t st, int sms) {
+cudaError_t launch(const CUtensorMap& tile, const CUtensorMap& edge, const CUtensorMap& w, const Pass& p, cudaStream_t st, int sms) {
   auto kernel = contract_kernel<OUT, GRAD>;
   const uint32_t smem = layout_of(p, OUT, GRAD).total;
   // set on every call: the attribute belongs to the device that is current
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (err != cudaSuccess) return err;
-  return launch_dependent(kernel, dim3(sms), dim3(kThreads), smem, st, tile, w, p);
+  return launch_dependent(kernel, dim3(sms), dim3(kThreads), smem, st, tile, edge, w, p);
 }
 
 }  // namespace
@@ -760,9 +840,11 @@ size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int
 cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
   const Plan q = plan_of(a.G, a.r, a.C, a.R_max, a.out != nullptr, a.grad != nullptr, sms);
   const Pass p = pass_of(a, q);
-  CUtensorMap tile, w;
+  CUtensorMap tile, edge, w;
   bool ok = encode_2d(&tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
-                      64, kTile, CU_TENSOR_MAP_SWIZZLE_128B);
+                      64, kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_2d(&edge, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
+                      64, kEdge, CU_TENSOR_MAP_SWIZZLE_128B);
   if (a.out) {
     // a group's matrix is a plane of its own, so that a box past its edge reads zeros
     const CUtensorMapSwizzle span = q.rp == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -775,9 +857,9 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
     w = tile;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (!a.grad) return launch<true, false>(tile, w, p, st, sms);
-  if (!a.out) return launch<false, true>(tile, w, p, st, sms);
-  return launch<true, true>(tile, w, p, st, sms);
+  if (!a.grad) return launch<true, false>(tile, edge, w, p, st, sms);
+  if (!a.out) return launch<false, true>(tile, edge, w, p, st, sms);
+  return launch<true, true>(tile, edge, w, p, st, sms);
 }
 
 cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
