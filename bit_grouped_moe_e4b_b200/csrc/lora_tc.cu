@@ -21,8 +21,9 @@
 // in that order, cut into equal runs for the CTAs, so that the groups' sizes do
 // not unbalance it; a CTA accumulates a group's gradient in TMEM over the
 // consecutive row tiles of its run, and writes it to its place when it took all
-// the group's tiles, else (the first and last of its run) to a part that
-// finish_kernel sums in CTA order: results depend on the sizes alone.
+// the group's tiles, else (the first and last of its run) to a part, with a note
+// of whose it is; finish_kernel sums the parts in CTA order: results depend on
+// the sizes alone.
 //   warp 0       TMA: W's box, and the tile's where its rows lie together (in
 //                boxes of 32 rows at a group's end)
 //   warp 1       TMEM and the single-thread MMA issue
@@ -56,6 +57,12 @@ constexpr int kMaxStages = 6;
 constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
 constexpr uint32_t kSmemLimit = 232448;
 
+// A part of a gradient: its group and column block, and whether it is the first
+// of the group's. group < 0: none.
+struct Note {
+  int32_t group, block, first;
+};
+
 struct Pass {
   int64_t C, R_max, rows, ld_z;
   const uint16_t* z;
@@ -66,6 +73,7 @@ struct Pass {
   const float* v;
   float* grad;
   float* grad_part;
+  Note* notes;  // of the parts, two a CTA
   int32_t* status;
   int G, r, rp;        // rp: the rank's operand width, 16, 32 or 64
   int blocks, chunks;  // column blocks; column tiles of a block
@@ -96,9 +104,8 @@ __host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, in
   return end > beg ? (end - beg + kTile - 1) / kTile : 0;
 }
 
-// First item of CTA b's run out of W items over n CTAs, and the CTA of an item.
+// First item of CTA b's run out of W items over n CTAs.
 __host__ __device__ inline int64_t run_start(int64_t W, int64_t n, int64_t b) { return b * W / n; }
-__host__ __device__ inline int64_t run_of(int64_t W, int64_t n, int64_t w) { return ((w + 1) * n - 1) / W; }
 
 // A position in the list of (column block, row tile), row tiles in group order.
 struct Walk {
@@ -229,6 +236,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   }
   const int64_t W = T * p.blocks;
   const int64_t n_run = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
+  if (GRAD && tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
   if (int64_t(blockIdx.x) >= n_run) return;  // uniform; also where no group has rows
   const int64_t w0 = run_start(W, n_run, blockIdx.x), w1 = run_start(W, n_run, int64_t(blockIdx.x) + 1);
   const int64_t rt0 = w0 % T;
@@ -602,6 +610,8 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           float* dst = direct ? p.grad + int64_t(wk.g) * p.C * p.r
                               : p.grad_part + (2 * int64_t(blockIdx.x) + (seg0 == 0 ? 0 : 1)) * block * p.r;
           const bool add = direct && p.accumulate;
+          if (!direct && m == 0)
+            p.notes[2 * blockIdx.x + (seg0 == 0 ? 0 : 1)] = Note{wk.g, wk.cb, whole_start};
           const int nc = chunks_of(wk.cb);
           for (int c = 0; c < nc; ++c) {
             const int64_t n = int64_t(c) * kTile + m;
@@ -668,80 +678,71 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
 }
 
 // The gradients that several CTAs share (the parts' sum, in CTA order) and
-// those of groups without rows (zero). CTA (x, y): piece x of a column block's
-// values of group y.
+// those of groups without rows (zero).
 struct Finish {
   Pass p;
-  int64_t grid;  // CTAs of the pass
+  int ctas;  // of the pass; 0 where there were no rows
 };
-constexpr int kFinishPieces = 4;
+constexpr int kFinishPieces = 4;  // CTAs of one gradient
 
-E4B_DEV void finish_one(const Finish& f, int piece, int g) {
+// The parts that begin in CTA b of the pass: each goes on in the first parts of
+// the CTAs after it.
+E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
   const Pass& p = f.p;
-  const int cb = piece / kFinishPieces, sub = piece % kFinishPieces;
-  __shared__ int64_t s_before[8], s_all[8];
-  const int tid = threadIdx.x;
-  int64_t beg, end, before = 0, all = 0;
-  for (int k = tid; k < p.G; k += 256) {
-    const int64_t t = group_tiles(p.offsets, k, p.R_max, beg, end);
-    all += t;
-    if (k < g) before += t;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, d);
-    all += __shfl_xor_sync(0xffffffffu, all, d);
-  }
-  __syncthreads();
-  if ((tid & 31) == 0) {
-    s_before[tid >> 5] = before;
-    s_all[tid >> 5] = all;
-  }
-  __syncthreads();
-  before = all = 0;
-  for (int k = 0; k < 8; ++k) {
-    before += s_before[k];
-    all += s_all[k];
-  }
-  const int64_t tiles = group_tiles(p.offsets, g, p.R_max, beg, end);
-  const int64_t W = all * p.blocks, n_run = W < f.grid ? W : f.grid;
-  int64_t b0 = 0, b1 = -1;
-  int slot0 = 0;  // b0's first or last part; the others end or lie within the group: their first
-  if (tiles) {
-    const int64_t w0 = cb * all + before;
-    b0 = run_of(W, n_run, w0);
-    slot0 = run_start(W, n_run, b0) < w0;
-    b1 = run_of(W, n_run, w0 + tiles - 1);
-    if (b0 == b1) return;  // that CTA wrote it
-  } else if (p.accumulate) {
-    return;
-  }
-  const int64_t block = int64_t(p.chunks) * kTile, c0 = cb * block;
-  const int cols = int(min(block, p.C - c0));
-  // values that lie together: the block's columns by r, or r rows of its columns
-  const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
-  float* dst = p.grad + int64_t(g) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
-  for (int i = sub * 256 + tid; i < lines * len4; i += 256 * kFinishPieces) {
-    const int line = i / len4, at = (i - line * len4) * 4;
-    float4* out = reinterpret_cast<float4*>(dst + line * p.C + at);
-    float4 s = p.accumulate ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* src = p.grad_part + line * block + at;
-    for (int64_t b = b0; b <= b1; ++b) {
-      const float4 v = *reinterpret_cast<const float4*>(src + (2 * b + (b == b0 ? slot0 : 0)) * block * p.r);
-      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  const int64_t block = int64_t(p.chunks) * kTile, part = block * p.r;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const Note note = p.notes[2 * b + k];
+    if (note.group < 0 || !note.first) continue;
+    int last = b;
+    while (last + 1 < f.ctas) {
+      const Note more = p.notes[2 * (last + 1)];
+      if (more.group != note.group || more.block != note.block || more.first) break;
+      ++last;
     }
-    *out = s;
+    const int64_t c0 = note.block * block;
+    const int cols = int(min(block, p.C - c0));
+    // values that lie together: the block's columns by r, or r rows of its columns
+    const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
+    float* dst = p.grad + int64_t(note.group) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
+    for (int i = piece * 256 + int(threadIdx.x); i < lines * len4; i += 256 * kFinishPieces) {
+      const int line = i / len4, at = (i - line * len4) * 4;
+      float4* out = reinterpret_cast<float4*>(dst + line * p.C + at);
+      float4 s = p.accumulate ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* src = p.grad_part + line * block + at;
+#pragma unroll 2
+      for (int c = b; c <= last; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (2 * c + (c == b ? k : 0)) * part);
+        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+      }
+      *out = s;
+    }
   }
 }
 
+E4B_DEV void finish_empty(const Finish& f, int g, int piece) {
+  const Pass& p = f.p;
+  int64_t beg, end;
+  if (p.accumulate || group_tiles(p.offsets, g, p.R_max, beg, end)) return;
+  const int64_t n4 = p.C * p.r / 4;
+  float4* dst = reinterpret_cast<float4*>(p.grad) + int64_t(g) * n4;
+  for (int64_t i = piece * 256 + threadIdx.x; i < n4; i += 256 * kFinishPieces) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// CTAs (x, y): of the first pass' parts, of the second's, of the groups.
 __global__ void __launch_bounds__(256)
 finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b) {
   grid_dependency_wait();
   grid_launch_dependents();
-  if (int(blockIdx.x) < a.p.blocks * kFinishPieces)
-    finish_one(a, blockIdx.x, blockIdx.y);
-  else
-    finish_one(b, blockIdx.x - a.p.blocks * kFinishPieces, blockIdx.y);
+  const int x = blockIdx.x;
+  if (x < a.ctas) {
+    finish_parts(a, x, blockIdx.y);
+  } else if (x < a.ctas + b.ctas) {
+    finish_parts(b, x - a.ctas, blockIdx.y);
+  } else {
+    finish_empty(a, x - a.ctas - b.ctas, blockIdx.y);
+    if (b.p.grad) finish_empty(b, x - a.ctas - b.ctas, blockIdx.y);
+  }
 }
 
 // ---------------------------------------------------------------- the plan
@@ -751,9 +752,10 @@ struct Plan {
 
 // Column tiles of a block: at most those whose gradients TMEM holds, and of
 // these the number with the least time by this estimate, in units of one tile's
-// 32 KB from HBM: the longest run's items (half a unit each besides their
-// tiles), the last gradients' way out of TMEM, the parts of `out` written and
-// read again. Row tiles are an estimate: groups may end anywhere in one.
+// 32 KB from HBM: the longest run's items (for each, besides its tiles, half a
+// unit, or with a gradient of a wide rank, whose terms have one buffer, more),
+// the last gradients' way out of TMEM, the parts of `out` written and read
+// again. Row tiles are an estimate: groups may end anywhere in one.
 Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
   Plan q;
   q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
@@ -763,12 +765,13 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   if (grad && most > kMaxChunks) most = kMaxChunks;
   const int64_t all = (C + kTile - 1) / kTile;
   const int64_t groups = G < R_max ? G : R_max;
-  const int64_t tiles = R_max / kTile + (groups + 1) / 2;  // > 0, if there are rows
+  int64_t tiles = R_max / kTile + (groups + 1) / 2;  // > 0, if there are rows
+  if (tiles < groups) tiles = groups;
   double best = 0;
   q.chunks = 0;
   for (int64_t c = 1; c <= most && c <= all; ++c) {
     const int64_t blocks = (all + c - 1) / c, items = blocks * tiles;
-    double t = double((items + sms - 1) / sms) * (double(c) + 0.5);
+    double t = double((items + sms - 1) / sms) * (double(c) + (grad && q.rp == 64 ? 2.5 : 0.5));
     if (grad) t += 0.5 * double(c);
     if (out && blocks > 1) t += double(items) * r / (32.0 * sms);
     if (!q.chunks || t <= best) {
@@ -785,7 +788,9 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   return q;
 }
 
-Pass pass_of(const ContractArgs& a, const Plan& q) {
+int64_t part_floats(int r, const Plan& q, int sms) { return int64_t(2) * sms * q.chunks * kTile * r; }
+
+Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   Pass p{};
   p.C = a.C;
   p.R_max = a.R_max;
@@ -799,6 +804,7 @@ Pass pass_of(const ContractArgs& a, const Plan& q) {
   p.v = a.v;
   p.grad = a.grad;
   p.grad_part = a.grad_part;
+  p.notes = a.grad ? reinterpret_cast<Note*>(a.grad_part + part_floats(a.r, q, sms)) : nullptr;
   p.status = a.status;
   p.G = a.G;
   p.r = a.r;
@@ -834,12 +840,12 @@ int contract_blocks(int G, int r, int64_t C, int64_t R_max, bool out, bool grad,
 }
 
 size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int sms) {
-  return size_t(2) * sms * plan_of(G, r, C, R_max, out, true, sms).chunks * kTile * r * 4;
+  return size_t(part_floats(r, plan_of(G, r, C, R_max, out, true, sms), sms)) * 4 + size_t(2) * sms * sizeof(Note);
 }
 
 cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
   const Plan q = plan_of(a.G, a.r, a.C, a.R_max, a.out != nullptr, a.grad != nullptr, sms);
-  const Pass p = pass_of(a, q);
+  const Pass p = pass_of(a, q, sms);
   CUtensorMap tile, edge, w;
   bool ok = encode_2d(&tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
                       64, kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
@@ -864,16 +870,15 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
 
 cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
   Finish f[2] = {};
-  int blocks = 0, i = 0, G = 0;
+  int ctas = a->G, i = 0;
   for (const ContractArgs* c : {a, b}) {
     if (!c) continue;
-    f[i].p = pass_of(*c, plan_of(c->G, c->r, c->C, c->R_max, c->out != nullptr, true, sms));
-    f[i].grid = sms;
-    blocks += f[i].p.blocks * kFinishPieces;
-    G = c->G;
+    f[i].p = pass_of(*c, plan_of(c->G, c->r, c->C, c->R_max, c->out != nullptr, true, sms), sms);
+    f[i].ctas = c->R_max > 0 ? sms : 0;
+    ctas += f[i].ctas;
     ++i;
   }
-  return launch_dependent(finish_kernel, dim3(unsigned(blocks), unsigned(G)), dim3(256), 0, st, f[0], f[1]);
+  return launch_dependent(finish_kernel, dim3(unsigned(ctas), kFinishPieces), dim3(256), 0, st, f[0], f[1]);
 }
 
 }  // namespace e4b
