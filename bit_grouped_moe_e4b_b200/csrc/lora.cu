@@ -54,8 +54,8 @@ E4B_DEV void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
 E4B_DEV uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 E4B_DEV uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Piece `index` of the groups' rows, cut into pieces of up to `piece`
-// positions in group order.
+// Piece `index` of the groups' rows: each group is cut into as few pieces of up
+// to `piece` positions (a multiple of 16) as there can be, of even sizes.
 struct Piece {
   int g;          // -1: no such piece
   int32_t row0;   // first position
@@ -88,7 +88,8 @@ E4B_DEV Piece find_piece(const int64_t* __restrict__ offsets, int G, int64_t R_m
     for (int g = lo; g < hi; ++g) {
       const int beg = clamped(g), n = max(clamped(g + 1) - beg, 0), np = (n + piece - 1) / piece;
       if (left < np) {
-        t = Piece{g, beg + int(left) * piece, min(piece, n - int(left) * piece)};
+        const int size = ((n + np - 1) / np + 15) / 16 * 16, at = int(left) * size;  // at most `piece`
+        t = Piece{g, beg + at, max(min(size, n - at), 0)};
         break;
       }
       left -= np;
@@ -206,15 +207,17 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 
 // ------------------------------------------------ expansions: y and dx
 // out_i = base_i + (w v[p]) W over C columns: W is B_g [C, r] with v = s, w =
-// w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. A CTA takes 128
-// positions of a group and eight warps' columns. It stages v's fragments (hi
-// and lo terms, in the order of the MMA's A operand) in shared memory once. A
-// warp owns two strips of 32 columns (adjacent, or a gate and an up strip),
-// keeps its columns of W in registers and walks the positions 16 at a time, the
-// rows of base of the next kAhead tiles under way (cp.async into the lane's own
-// slots of shared memory: no barrier). Column c of n8-tile i of a strip is the
-// strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results are eight
-// consecutive columns: one 16-byte access to base, y and h.
+// w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. A CTA takes a piece of a
+// group's positions and eight warps' columns. It stages v's fragments (hi and lo
+// terms, in the order of the MMA's A operand) in shared memory once. A warp owns
+// two strips of 32 columns (adjacent, or a gate and an up strip), keeps its
+// columns of W in registers and walks the positions 16 at a time, the rows of
+// base of the next kAhead tiles under way (cp.async into the lane's own slots of
+// shared memory: no barrier). Column c of n8-tile i of a strip is the strip's
+// column 8 (c / 2) + 2 i + c % 2, so that a lane's results are eight consecutive
+// columns: one 16-byte access to base, y and h. Bound by HBM, and next by the
+// instructions that unpack, add and pack 16 bytes a lane: larger pieces spread
+// a CTA's start (the piece, W, v) over more rows.
 struct Expand {
   const uint16_t* w;
   bool scaled;
@@ -229,12 +232,10 @@ struct Expand {
   int slices;
   float* v_out;    // the slices' sum, written by the first columns' CTAs; or null
   int col_blocks;
-  int act;
+  int piece;       // positions of a piece
   float alpha, limit;
 };
 
-constexpr int kExpandRows = 128;  // positions of a piece
-constexpr int kExpandTiles = kExpandRows / 16;
 constexpr int kAhead = 3;  // tiles of base under way
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
@@ -242,11 +243,11 @@ enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
 E4B_DEV void add8(float (&v)[8], uint4 w) {
   const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2(q[i]);
-    v[2 * i] += f.x;
-    v[2 * i + 1] += f.y;
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(v[2 * i]), "+f"(v[2 * i + 1])
+        : "r"(q[i] << 16), "r"(q[i] & 0xFFFF0000u));
 }
 
 E4B_DEV uint4 pack8(const float (&a)[8]) {
@@ -266,13 +267,15 @@ E4B_DEV float4 sum_slices(const Adapters& d, const Expand& e, int32_t p, int j) 
   return v;
 }
 
-// KS: MMA k-steps over the rank (r <= 16 KS).
-template <int KS, int GLU, bool WT>
+// KS: MMA k-steps over the rank (r <= 16 KS); ACT: the activation behind GLU.
+template <int KS, int GLU, int ACT, bool WT>
 __global__ void __launch_bounds__(kThreads, KS > 2 ? 1 : 2)
 expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand e) {
-  extern __shared__ uint4 ring[];  // [kAhead + 1][2][2][kThreads], base alone
-  __shared__ uint4 frags[kExpandTiles][KS][2][32];
-  __shared__ int32_t at[kExpandRows];
+  extern __shared__ uint4 smem[];
+  using Frags = uint4[KS][2][32];
+  Frags* frags = reinterpret_cast<Frags*>(smem);                 // [piece / 16]
+  uint4* ring = smem + e.piece / 16 * (KS * 64);                 // [kAhead + 1][2][2][kThreads], with base
+  int32_t* at = reinterpret_cast<int32_t*>(ring + (e.base ? (kAhead + 1) * 4 * kThreads : 0));  // [piece]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q = lane & 3, rr = lane >> 2;
   const FlatBlock fb = flat_block(e.col_blocks);
@@ -280,8 +283,8 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   const int64_t half = e.C / 2;
   const int64_t col0[2] = {block_col, GLU == kGluHalves ? half + block_col : block_col + 32};  // the strips
   const int64_t limit[2] = {GLU == kGluHalves ? half : e.C, e.C};
-  const Piece t = find_piece(d.offsets, d.G, d.R_max, kExpandRows, fb.piece);
-  if (t.g < 0) {
+  const Piece t = find_piece(d.offsets, d.G, d.R_max, e.piece, fb.piece);
+  if (t.g < 0 || t.n == 0) {
     grid_dependency_wait();  // the grid must not complete before the launch it depends on
     return;
   }
@@ -327,7 +330,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   grid_dependency_wait();
   grid_launch_dependents();
 
-  for (int i = threadIdx.x; i < kExpandRows; i += kThreads) at[i] = i < t.n ? row_of(d.row, d.rows, t.row0 + i) : -1;
+  for (int i = threadIdx.x; i < (t.n + 15) / 16 * 16; i += kThreads) at[i] = i < t.n ? row_of(d.row, d.rows, t.row0 + i) : -1;
   const int tiles = (t.n + 15) / 16;
   for (int i = threadIdx.x; i < tiles * KS * 32; i += kThreads) {
     const int l = i & 31, ks = (i >> 5) % KS, tile = (i >> 5) / KS;
@@ -400,14 +403,14 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
       if constexpr (GLU == kGluHalves) {
         float h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = glu_act(e.act, v[0][k], v[1][k], e.alpha, e.limit);
+        for (int k = 0; k < 8; ++k) h[k] = glu_act(ACT, v[0][k], v[1][k], e.alpha, e.limit);
         if (in[0]) *reinterpret_cast<uint4*>(e.h + int64_t(row) * e.ld_h + c[0]) = pack8(h);
       } else if constexpr (GLU == kGluInterleaved) {
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           float h[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] = glu_act(e.act, v[st][2 * k], v[st][2 * k + 1], e.alpha, e.limit);
+          for (int k = 0; k < 4; ++k) h[k] = glu_act(ACT, v[st][2 * k], v[st][2 * k + 1], e.alpha, e.limit);
           if (in[st])
             *reinterpret_cast<uint2*>(e.h + int64_t(row) * e.ld_h + c[st] / 2) =
                 make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
@@ -487,17 +490,37 @@ int forward_slices(int G, int r, int64_t K, int64_t R_max, int sms) {
   return int(want < 1 ? 1 : want);
 }
 
-template <int GLU, bool WT>
-cudaError_t launch_expand_as(const Adapters& d, Expand e, cudaStream_t st) {
+// Positions of an expansion's piece: the largest that leaves the GPU four waves
+// of CTAs, and whose fragments leave room for two CTAs an SM.
+int expand_piece(int64_t G, int64_t R_max, int64_t col_blocks, int KS, int sms) {
+  int piece = KS == 1 ? 512 : KS == 2 ? 256 : 128;
+  while (piece > 128 && (R_max / piece + (G < R_max ? G : R_max) / 2) * col_blocks < int64_t(sms) * 8) piece /= 2;
+  return piece;
+}
+
+template <int GLU, int ACT, bool WT>
+cudaError_t launch_expand_as(const Adapters& d, Expand e, cudaStream_t st, int sms) {
   const int64_t cols = GLU == kGluHalves ? e.C / 2 : e.C, per = kWarps * (GLU == kGluHalves ? 32 : 64);
+  const int KS = d.r <= 16 ? 1 : d.r <= 32 ? 2 : 4;
   e.col_blocks = int((cols + per - 1) / per);
-  const dim3 grid(unsigned(e.col_blocks * pieces_bound(d.G, d.R_max, kExpandRows)));
-  auto kernel = d.r <= 16 ? expand_kernel<1, GLU, WT> : d.r <= 32 ? expand_kernel<2, GLU, WT> : expand_kernel<4, GLU, WT>;
-  const int smem = e.base ? (kAhead + 1) * 4 * kThreads * 16 : 0;
+  e.piece = expand_piece(d.G, d.R_max, e.col_blocks, KS, sms);
+  const dim3 grid(unsigned(e.col_blocks * pieces_bound(d.G, d.R_max, e.piece)));
+  auto kernel = KS == 1 ? expand_kernel<1, GLU, ACT, WT> : KS == 2 ? expand_kernel<2, GLU, ACT, WT> : expand_kernel<4, GLU, ACT, WT>;
+  const int smem = e.piece / 16 * KS * 1024 + (e.base ? (kAhead + 1) * 4 * kThreads * 16 : 0) + e.piece * 4;
   // set on every call: the attribute belongs to the device that is current
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, grid, dim3(kThreads), smem, st, d, e);
+}
+
+cudaError_t launch_expand(const Adapters& d, const Expand& e, int layout, int act, cudaStream_t st, int sms) {
+  if (!e.h) return launch_expand_as<kGluNone, 0, false>(d, e, st, sms);
+  const bool clamped = act == E4B_ACT_CLAMPED_GLU;
+  if (layout == E4B_GATE_UP_INTERLEAVED)
+    return clamped ? launch_expand_as<kGluInterleaved, E4B_ACT_CLAMPED_GLU, false>(d, e, st, sms)
+                   : launch_expand_as<kGluInterleaved, E4B_ACT_SWIGLU, false>(d, e, st, sms);
+  return clamped ? launch_expand_as<kGluHalves, E4B_ACT_CLAMPED_GLU, false>(d, e, st, sms)
+                 : launch_expand_as<kGluHalves, E4B_ACT_SWIGLU, false>(d, e, st, sms);
 }
 
 template <int JT>
@@ -555,12 +578,10 @@ cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaSt
   if (err != cudaSuccess) return err;
   *launches = 1;
   if (!a.y && !a.h && slices == 1) return cudaSuccess;  // s alone was asked for
-  Expand e{a.b, true, a.N, a.base, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, slices > 1 ? a.s : nullptr, 0,
-           a.activation, a.glu_alpha, a.glu_limit};
+  const Expand e{a.b, true, a.N, a.base, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, slices > 1 ? a.s : nullptr,
+                 0, 0, a.glu_alpha, a.glu_limit};
   *launches = 2;
-  if (!a.h) return launch_expand_as<kGluNone, false>(d, e, st);
-  if (a.gate_up_layout == E4B_GATE_UP_INTERLEAVED) return launch_expand_as<kGluInterleaved, false>(d, e, st);
-  return launch_expand_as<kGluHalves, false>(d, e, st);
+  return launch_expand(d, e, a.gate_up_layout, a.activation, st, sms);
 }
 
 cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flags, cudaStream_t st, int sms,
@@ -613,7 +634,7 @@ cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flag
     }
     if (a.dx) {
       const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1, nullptr, 0, 0, 0.f, 0.f};
-      if ((err = launch_expand_as<kGluNone, true>(d, e, st)) != cudaSuccess) return err;
+      if ((err = launch_expand_as<kGluNone, 0, true>(d, e, st, sms)) != cudaSuccess) return err;
       ++*launches;
     }
   }

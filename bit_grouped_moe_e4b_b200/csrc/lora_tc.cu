@@ -683,7 +683,6 @@ struct Finish {
   Pass p;
   int ctas;  // of the pass; 0 where there were no rows
 };
-constexpr int kFinishPieces = 4;  // CTAs of one gradient
 
 // The parts that begin in CTA b of the pass: each goes on in the first parts of
 // the CTAs after it.
@@ -705,7 +704,7 @@ E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
     // values that lie together: the block's columns by r, or r rows of its columns
     const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
     float* dst = p.grad + int64_t(note.group) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
-    for (int i = piece * 256 + int(threadIdx.x); i < lines * len4; i += 256 * kFinishPieces) {
+    for (int i = piece * 256 + int(threadIdx.x); i < lines * len4; i += 256 * int(gridDim.y)) {
       const int line = i / len4, at = (i - line * len4) * 4;
       float4* out = reinterpret_cast<float4*>(dst + line * p.C + at);
       float4 s = p.accumulate ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -726,7 +725,7 @@ E4B_DEV void finish_empty(const Finish& f, int g, int piece) {
   if (p.accumulate || group_tiles(p.offsets, g, p.R_max, beg, end)) return;
   const int64_t n4 = p.C * p.r / 4;
   float4* dst = reinterpret_cast<float4*>(p.grad) + int64_t(g) * n4;
-  for (int64_t i = piece * 256 + threadIdx.x; i < n4; i += 256 * kFinishPieces) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t i = piece * 256 + threadIdx.x; i < n4; i += 256 * gridDim.y) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // CTAs (x, y): of the first pass' parts, of the second's, of the groups.
@@ -870,15 +869,18 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
 
 cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
   Finish f[2] = {};
-  int ctas = a->G, i = 0;
+  int ctas = a->G, i = 0, most = 0;
   for (const ContractArgs* c : {a, b}) {
     if (!c) continue;
     f[i].p = pass_of(*c, plan_of(c->G, c->r, c->C, c->R_max, c->out != nullptr, true, sms), sms);
     f[i].ctas = c->R_max > 0 ? sms : 0;
     ctas += f[i].ctas;
+    if (most < f[i].p.chunks) most = f[i].p.chunks;
     ++i;
   }
-  return launch_dependent(finish_kernel, dim3(unsigned(ctas), kFinishPieces), dim3(256), 0, st, f[0], f[1]);
+  // a part's values over CTAs, four a thread
+  const int pieces = (most * kTile * a->r + 4095) / 4096;
+  return launch_dependent(finish_kernel, dim3(unsigned(ctas), unsigned(pieces)), dim3(256), 0, st, f[0], f[1]);
 }
 
 }  // namespace e4b
