@@ -22,6 +22,7 @@
 #include "adapters.h"
 #include "common.cuh"
 #include "lora_tc.h"
+#include "lora_walk.cuh"
 #include "sm100.cuh"
 
 namespace e4b {
@@ -54,8 +55,8 @@ E4B_DEV void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
 E4B_DEV uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 E4B_DEV uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Piece `index` of the groups' rows: each group is cut into as few pieces of up
-// to `piece` positions (a multiple of 16) as there can be, of even sizes.
+// Piece `index` of the groups' rows, cut into pieces of up to `piece`
+// positions in group order.
 struct Piece {
   int g;          // -1: no such piece
   int32_t row0;   // first position
@@ -88,8 +89,7 @@ E4B_DEV Piece find_piece(const int64_t* __restrict__ offsets, int G, int64_t R_m
     for (int g = lo; g < hi; ++g) {
       const int beg = clamped(g), n = max(clamped(g + 1) - beg, 0), np = (n + piece - 1) / piece;
       if (left < np) {
-        const int size = ((n + np - 1) / np + 15) / 16 * 16, at = int(left) * size;  // at most `piece`
-        t = Piece{g, beg + at, max(min(size, n - at), 0)};
+        t = Piece{g, beg + int(left) * piece, min(piece, n - int(left) * piece)};
         break;
       }
       left -= np;
@@ -106,16 +106,6 @@ E4B_DEV int32_t row_of(const int32_t* __restrict__ row, int64_t rows, int32_t p)
   if (!row) return p;
   const int32_t i = __ldg(row + p);
   return i >= 0 && i < rows ? i : -1;
-}
-
-// CTA b of a flat grid: column block b % blocks of piece b / blocks (the
-// pieces may pass the 65535 that the grid's second dimension holds).
-struct FlatBlock {
-  int col, piece;
-};
-E4B_DEV FlatBlock flat_block(int blocks) {
-  const int p = int(blockIdx.x) / blocks;
-  return FlatBlock{int(blockIdx.x) - p * blocks, p};
 }
 
 struct Adapters {
@@ -207,17 +197,16 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 
 // ------------------------------------------------ expansions: y and dx
 // out_i = base_i + (w v[p]) W over C columns: W is B_g [C, r] with v = s, w =
-// w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. A CTA takes a piece of a
-// group's positions and eight warps' columns. It stages v's fragments (hi and lo
-// terms, in the order of the MMA's A operand) in shared memory once. A warp owns
-// two strips of 32 columns (adjacent, or a gate and an up strip), keeps its
-// columns of W in registers and walks the positions 16 at a time, the rows of
-// base of the next kAhead tiles under way (cp.async into the lane's own slots of
-// shared memory: no barrier). Column c of n8-tile i of a strip is the strip's
-// column 8 (c / 2) + 2 i + c % 2, so that a lane's results are eight consecutive
-// columns: one 16-byte access to base, y and h. Bound by HBM, and next by the
-// instructions that unpack, add and pack 16 bytes a lane: larger pieces spread
-// a CTA's start (the piece, W, v) over more rows.
+// w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. Persistent CTAs walk
+// equal runs of the list of (columns of eight warps, tile of 128 positions). A
+// warp owns two strips of 32 columns (adjacent, or a gate and an up strip), keeps
+// its columns of W in registers while the group lasts, and takes a tile's
+// positions 16 at a time, the rows of base of the next kAhead sixteens under way,
+// past the end of the tile too (cp.async into the lane's own slots of shared
+// memory: no barrier). v's fragments (hi and lo terms, in the order of the MMA's
+// A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
+// strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
+// are eight consecutive columns: one 16-byte access to base, y and h.
 struct Expand {
   const uint16_t* w;
   bool scaled;
@@ -232,22 +221,29 @@ struct Expand {
   int slices;
   float* v_out;    // the slices' sum, written by the first columns' CTAs; or null
   int col_blocks;
-  int piece;       // positions of a piece
   float alpha, limit;
 };
 
-constexpr int kAhead = 3;  // tiles of base under way
+constexpr int kAhead = 3;  // sixteens of base under way
+constexpr int kSixteens = kTile / 16;
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
 
-E4B_DEV void add8(float (&v)[8], uint4 w) {
-  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
-        "mov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(v[2 * i]), "+f"(v[2 * i + 1])
-        : "r"(q[i] << 16), "r"(q[i] & 0xFFFF0000u));
+// The activation of an expanded pair, in six instructions a value for SwiGLU:
+// exp2 and the reciprocal without their handling of denormals (which took 16,
+// and the kernel's time with them). Where the reciprocal flushes to zero the
+// exact factor is under 2^-125.
+template <int ACT>
+E4B_DEV float activate(float g, float u, float alpha, float limit) {
+  if constexpr (ACT == E4B_ACT_CLAMPED_GLU) {
+    g = g > limit ? limit : g;
+    u = (u > limit ? limit : (u < -limit ? -limit : u)) + 1.f;
+  }
+  const float slope = ACT == E4B_ACT_CLAMPED_GLU ? alpha : 1.f;
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (slope * -1.4426950408889634f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return (g * u) * s;
 }
 
 E4B_DEV uint4 pack8(const float (&a)[8]) {
@@ -258,9 +254,9 @@ E4B_DEV uint4 pack8(const float (&a)[8]) {
 // Four values of position p, j .. j + 3: the slices' sum.
 E4B_DEV float4 sum_slices(const Adapters& d, const Expand& e, int32_t p, int j) {
   const float* at = e.v + int64_t(p) * d.r + j;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v = *reinterpret_cast<const float4*>(at);
 #pragma unroll 4
-  for (int k = 0; k < e.slices; ++k) {
+  for (int k = 1; k < e.slices; ++k) {
     const float4 z = *reinterpret_cast<const float4*>(at + int64_t(k) * d.R_max * d.r);
     v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
   }
@@ -271,152 +267,241 @@ E4B_DEV float4 sum_slices(const Adapters& d, const Expand& e, int32_t p, int j) 
 template <int KS, int GLU, int ACT, bool WT>
 __global__ void __launch_bounds__(kThreads, KS > 2 ? 1 : 2)
 expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand e) {
+  struct Item {
+    int32_t g, cb, row0, n;
+  };
   extern __shared__ uint4 smem[];
-  using Frags = uint4[KS][2][32];
-  Frags* frags = reinterpret_cast<Frags*>(smem);                 // [piece / 16]
-  uint4* ring = smem + e.piece / 16 * (KS * 64);                 // [kAhead + 1][2][2][kThreads], with base
-  int32_t* at = reinterpret_cast<int32_t*>(ring + (e.base ? (kAhead + 1) * 4 * kThreads : 0));  // [piece]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using Frags = uint4[kSixteens][KS][2][32];
+  Frags* frags = reinterpret_cast<Frags*>(smem);                 // [2]
+  uint4* ring = smem + 2 * sizeof(Frags) / sizeof(uint4);        // [kAhead + 1][2][2][kThreads], with base
+  __shared__ int32_t at[2][kTile];
+  __shared__ Item items[3];
+  __shared__ int64_t s_sum[kWarps], s_start[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q = lane & 3, rr = lane >> 2;
-  const FlatBlock fb = flat_block(e.col_blocks);
-  const int64_t block_col = (int64_t(fb.col) * kWarps + warp) * (GLU == kGluHalves ? 32 : 64);
   const int64_t half = e.C / 2;
-  const int64_t col0[2] = {block_col, GLU == kGluHalves ? half + block_col : block_col + 32};  // the strips
   const int64_t limit[2] = {GLU == kGluHalves ? half : e.C, e.C};
-  const Piece t = find_piece(d.offsets, d.G, d.R_max, e.piece, fb.piece);
-  if (t.g < 0 || t.n == 0) {
+  // first columns of the warp's strips
+  auto strip = [&](int cb, int st) {
+    const int64_t c = (int64_t(cb) * kWarps + warp) * (GLU == kGluHalves ? 32 : 64);
+    return GLU == kGluHalves ? st * half + c : c + 32 * st;
+  };
+
+  const Run run = find_run<kThreads>(d.offsets, d.G, d.R_max, e.col_blocks, s_sum, s_start);
+  if (run.count == 0) {
     grid_dependency_wait();  // the grid must not complete before the launch it depends on
     return;
   }
-
-  // W does not come from the launch before this one, which has itself waited
-  // for all earlier work
-  uint32_t bf[2][4][KS][2];
-  const uint16_t* wg = e.w + int64_t(t.g) * e.C * d.r;
-#pragma unroll
-  for (int st = 0; st < 2; ++st) {
-    if constexpr (WT) {
-      const int64_t n = col0[st] + 8 * (rr >> 1);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int j = 16 * ks + 4 * q;
-        uint4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = n < limit[st] && j + k < d.r ? ldg16(wg + int64_t(j + k) * e.C + n) : make_uint4(0, 0, 0, 0);
-        const uint32_t sel = rr & 1 ? 0x7632 : 0x5410;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bf[st][i][ks][0] = prmt(word(v[0], i), word(v[1], i), sel);
-          bf[st][i][ks][1] = prmt(word(v[2], i), word(v[3], i), sel);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t n = col0[st] + 8 * (rr >> 1) + 2 * i + (rr & 1);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int j = 16 * ks + 4 * q;
-          uint2 v = make_uint2(0, 0);
-          if (n < limit[st] && j < d.r) v = __ldg(reinterpret_cast<const uint2*>(wg + n * d.r + j));
-          bf[st][i][ks][0] = v.x;
-          bf[st][i][ks][1] = v.y;
-        }
-      }
-    }
-  }
-  const float w = e.scaled && d.scale ? __ldg(d.scale + t.g) : 1.f;
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  for (int i = threadIdx.x; i < (t.n + 15) / 16 * 16; i += kThreads) at[i] = i < t.n ? row_of(d.row, d.rows, t.row0 + i) : -1;
-  const int tiles = (t.n + 15) / 16;
-  for (int i = threadIdx.x; i < tiles * KS * 32; i += kThreads) {
-    const int l = i & 31, ks = (i >> 5) % KS, tile = (i >> 5) / KS;
-    const int m = 16 * tile + (l >> 2), j = 16 * ks + 4 * (l & 3);
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {  // rows m and m + 8: registers k and k + 2
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m + 8 * k < t.n && j < d.r) {
-        v = sum_slices(d, e, t.row0 + m + 8 * k, j);
-        if (e.v_out && fb.col == 0)
-          *reinterpret_cast<float4*>(e.v_out + int64_t(t.row0 + m + 8 * k) * d.r + j) = v;
-      }
-      split2(w * v.x, w * v.y, hi[k], lo[k]);
-      split2(w * v.z, w * v.w, hi[k + 2], lo[k + 2]);
-    }
-    frags[tile][ks][0][l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    frags[tile][ks][1][l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  Walk wk(d.offsets, d.G, d.R_max, run, s_start);  // thread 0's: the item after the next
+  auto note = [&](int64_t k) {
+    items[k % 3] = Item{wk.g, wk.cb, int32_t(wk.row0()), wk.n()};
+    if (k + 1 < run.count) wk.next();
+  };
+  if (tid == 0) {
+    note(0);
+    if (run.count > 1) note(1);
   }
   __syncthreads();
 
-  const int64_t c[2] = {col0[0] + 8 * q, col0[1] + 8 * q};
-  const bool in[2] = {c[0] < limit[0], c[1] < limit[1]};
-  if (!e.y && !e.h) return;
-  auto slot = [&](int tile, int i, int st) { return ring + ((tile % (kAhead + 1) * 2 + i) * 2 + st) * kThreads + threadIdx.x; };
-  auto fetch = [&](int tile) {
-    if (e.base && tile < tiles) {
+  uint32_t bf[2][4][KS][2];
+  auto load_w = [&](const Item& t) {
+    const uint16_t* wg = e.w + int64_t(t.g) * e.C * d.r;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      if constexpr (WT) {
+        const int64_t n = strip(t.cb, st) + 8 * (rr >> 1);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int j = 16 * ks + 4 * q;
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = n < limit[st] && j + k < d.r ? ldg16(wg + int64_t(j + k) * e.C + n) : make_uint4(0, 0, 0, 0);
+          const uint32_t sel = rr & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bf[st][i][ks][0] = prmt(word(v[0], i), word(v[1], i), sel);
+            bf[st][i][ks][1] = prmt(word(v[2], i), word(v[3], i), sel);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t n = strip(t.cb, st) + 8 * (rr >> 1) + 2 * i + (rr & 1);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const int j = 16 * ks + 4 * q;
+            uint2 v = make_uint2(0, 0);
+            if (n < limit[st] && j < d.r) v = __ldg(reinterpret_cast<const uint2*>(wg + n * d.r + j));
+            bf[st][i][ks][0] = v.x;
+            bf[st][i][ks][1] = v.y;
+          }
+        }
+      }
+    }
+  };
+  // v's share of this thread: KS places of the tile's fragments, four values of
+  // two rows each; and the row of position tid
+  float4 vr[KS][2];
+  float vw = 1.f;
+  int32_t vrow = -1;
+  auto load_v = [&](const Item& t) {
+    vw = e.scaled && d.scale ? __ldg(d.scale + t.g) : 1.f;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      const int i = u * kThreads + tid, ks = (i >> 5) % KS, six = (i >> 5) / KS;
+      const int m = 16 * six + (lane >> 2), j = 16 * ks + 4 * q;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // rows m and m + 8
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m + 8 * k < t.n && j < d.r) {
+          v = sum_slices(d, e, t.row0 + m + 8 * k, j);
+          if (e.v_out && t.cb == 0) *reinterpret_cast<float4*>(e.v_out + int64_t(t.row0 + m + 8 * k) * d.r + j) = v;
+        }
+        vr[u][k] = v;
+      }
+    }
+    if (tid < kTile) vrow = tid < t.n ? row_of(d.row, d.rows, t.row0 + tid) : -1;
+  };
+  auto store_v = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      const int i = u * kThreads + tid, ks = (i >> 5) % KS, six = (i >> 5) / KS;
+      uint4 hi, lo;  // registers k and k + 2: row m + 8 k
+      split2(vw * vr[u][0].x, vw * vr[u][0].y, hi.x, lo.x);
+      split2(vw * vr[u][1].x, vw * vr[u][1].y, hi.y, lo.y);
+      split2(vw * vr[u][0].z, vw * vr[u][0].w, hi.z, lo.z);
+      split2(vw * vr[u][1].z, vw * vr[u][1].w, hi.w, lo.w);
+      frags[buf][six][ks][0][lane] = hi;
+      frags[buf][six][ks][1][lane] = lo;
+    }
+    if (tid < kTile) at[buf][tid] = vrow;
+  };
+
+  // W does not come from the launch before this one, which has itself waited
+  // for all earlier work
+  Item t = items[0];
+  load_w(t);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_v(t);
+  store_v(0);
+  __syncthreads();
+
+  int asked = 0, taken = 0;  // sixteens of base: asked for, and used
+  auto slot = [&](int k, int i, int st) { return ring + ((k % (kAhead + 1) * 2 + i) * 2 + st) * kThreads + tid; };
+  auto fetch = [&](int buf, int six, int cb) {
+    if (e.base) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int32_t row = at[16 * tile + rr + 8 * i];
-        if (row < 0) continue;
+        const int32_t row = at[buf][16 * six + rr + 8 * i];
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
-          if (in[st]) sm100::cp_async_16(slot(tile, i, st), e.base + int64_t(row) * e.ld_base + c[st], 16);
+        for (int st = 0; st < 2; ++st) {
+          const int64_t c = strip(cb, st) + 8 * q;
+          if (row >= 0 && c < limit[st]) sm100::cp_async_16(slot(asked, i, st), e.base + int64_t(row) * e.ld_base + c, 16);
+        }
       }
     }
     sm100::cp_async_commit();
+    ++asked;
   };
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) fetch(k);
-  for (int tile = 0; tile < tiles; ++tile) {
-    fetch(tile + kAhead);
-    float acc[2][4][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint4 f = frags[tile][ks][part][lane];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma_bf16(acc[st][i], f.x, f.y, f.z, f.w, bf[st][i][ks][0], bf[st][i][ks][1]);
+  auto arrived = [&]() {  // the oldest sixteen
+    const int later = asked - taken - 1;
+    if (later >= 3) sm100::cp_async_wait<3>();
+    else if (later == 2) sm100::cp_async_wait<2>();
+    else if (later == 1) sm100::cp_async_wait<1>();
+    else sm100::cp_async_wait<0>();
+  };
+
+  int had = 0;  // sixteens of this item already asked for
+  for (int64_t k = 0; k < run.count; ++k) {
+    const int buf = int(k & 1);
+    const bool more = k + 1 < run.count;
+    Item next = t;
+    if (more) {
+      next = items[(k + 1) % 3];
+      load_v(next);
+    }
+    const int sixteens = (t.n + 15) / 16, next_sixteens = (next.n + 15) / 16;
+    const int stage_at = sixteens > kAhead ? sixteens - kAhead : 0;  // from here on the next item's rows are asked for
+    int next_had = 0;
+    while (had < sixteens && had < kAhead) fetch(buf, had++, t.cb);
+    const int64_t c[2] = {strip(t.cb, 0) + 8 * q, strip(t.cb, 1) + 8 * q};
+    const bool in[2] = {c[0] < limit[0], c[1] < limit[1]};
+    for (int six = 0; six < sixteens; ++six) {
+      if (more && six == stage_at) {
+        __syncthreads();  // all warps are past the item that used these fragments
+        store_v(buf ^ 1);
+        if (tid == 0 && k + 2 < run.count) note(k + 2);
+        __syncthreads();
       }
-    sm100::cp_async_wait<kAhead>();
+      if (had < sixteens)
+        fetch(buf, had++, t.cb);
+      else if (more && next_had < next_sixteens && next_had < kAhead)
+        fetch(buf ^ 1, next_had++, next.cb);
+      arrived();
+      int32_t row[2];
+      float acc[2][4][4];  // starts as base
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int32_t row = at[16 * tile + rr + 8 * i];
-      if (row < 0) continue;
-      float v[2][8];
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[st][2 * k] = acc[st][k][2 * i];
-          v[st][2 * k + 1] = acc[st][k][2 * i + 1];
-        }
-        if (e.base && in[st]) add8(v[st], *slot(tile, i, st));
-        if (e.y && in[st]) *reinterpret_cast<uint4*>(e.y + int64_t(row) * e.ld_y + c[st]) = pack8(v[st]);
-      }
-      if constexpr (GLU == kGluHalves) {
-        float h[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = glu_act(ACT, v[0][k], v[1][k], e.alpha, e.limit);
-        if (in[0]) *reinterpret_cast<uint4*>(e.h + int64_t(row) * e.ld_h + c[0]) = pack8(h);
-      } else if constexpr (GLU == kGluInterleaved) {
+      for (int i = 0; i < 2; ++i) {
+        row[i] = at[buf][16 * six + rr + 8 * i];
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-          float h[4];
+          const uint4 b = e.base && in[st] && row[i] >= 0 ? *slot(taken, i, st) : make_uint4(0, 0, 0, 0);
+          const uint32_t words[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] = glu_act(ACT, v[st][2 * k], v[st][2 * k + 1], e.alpha, e.limit);
-          if (in[st])
-            *reinterpret_cast<uint2*>(e.h + int64_t(row) * e.ld_h + c[st] / 2) =
-                make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+          for (int p = 0; p < 4; ++p) {
+            const float2 f = unpack2(words[p]);
+            acc[st][p][2 * i] = f.x;
+            acc[st][p][2 * i + 1] = f.y;
+          }
+        }
+      }
+      ++taken;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint4 f = frags[buf][six][ks][part][lane];
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[st][i], f.x, f.y, f.z, f.w, bf[st][i][ks][0], bf[st][i][ks][1]);
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (row[i] < 0) continue;
+        float v[2][8];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            v[st][2 * p] = acc[st][p][2 * i];
+            v[st][2 * p + 1] = acc[st][p][2 * i + 1];
+          }
+          if (e.y && in[st]) *reinterpret_cast<uint4*>(e.y + int64_t(row[i]) * e.ld_y + c[st]) = pack8(v[st]);
+        }
+        if constexpr (GLU == kGluHalves) {
+          float h[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) h[p] = activate<ACT>(v[0][p], v[1][p], e.alpha, e.limit);
+          if (in[0]) *reinterpret_cast<uint4*>(e.h + int64_t(row[i]) * e.ld_h + c[0]) = pack8(h);
+        } else if constexpr (GLU == kGluInterleaved) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            float h[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) h[p] = activate<ACT>(v[st][2 * p], v[st][2 * p + 1], e.alpha, e.limit);
+            if (in[st])
+              *reinterpret_cast<uint2*>(e.h + int64_t(row[i]) * e.ld_h + c[st] / 2) =
+                  make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+          }
         }
       }
     }
+    if (next.g != t.g || next.cb != t.cb) load_w(next);
+    t = next;
+    had = next_had;
   }
 }
 
@@ -490,27 +575,19 @@ int forward_slices(int G, int r, int64_t K, int64_t R_max, int sms) {
   return int(want < 1 ? 1 : want);
 }
 
-// Positions of an expansion's piece: the largest that leaves the GPU four waves
-// of CTAs, and whose fragments leave room for two CTAs an SM.
-int expand_piece(int64_t G, int64_t R_max, int64_t col_blocks, int KS, int sms) {
-  int piece = KS == 1 ? 512 : KS == 2 ? 256 : 128;
-  while (piece > 128 && (R_max / piece + (G < R_max ? G : R_max) / 2) * col_blocks < int64_t(sms) * 8) piece /= 2;
-  return piece;
-}
-
 template <int GLU, int ACT, bool WT>
 cudaError_t launch_expand_as(const Adapters& d, Expand e, cudaStream_t st, int sms) {
   const int64_t cols = GLU == kGluHalves ? e.C / 2 : e.C, per = kWarps * (GLU == kGluHalves ? 32 : 64);
   const int KS = d.r <= 16 ? 1 : d.r <= 32 ? 2 : 4;
   e.col_blocks = int((cols + per - 1) / per);
-  e.piece = expand_piece(d.G, d.R_max, e.col_blocks, KS, sms);
-  const dim3 grid(unsigned(e.col_blocks * pieces_bound(d.G, d.R_max, e.piece)));
+  int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, kTile);
+  if (grid > int64_t(sms) * (KS > 2 ? 1 : 2)) grid = int64_t(sms) * (KS > 2 ? 1 : 2);
   auto kernel = KS == 1 ? expand_kernel<1, GLU, ACT, WT> : KS == 2 ? expand_kernel<2, GLU, ACT, WT> : expand_kernel<4, GLU, ACT, WT>;
-  const int smem = e.piece / 16 * KS * 1024 + (e.base ? (kAhead + 1) * 4 * kThreads * 16 : 0) + e.piece * 4;
+  const int smem = 2 * kSixteens * KS * 64 * 16 + (e.base ? (kAhead + 1) * 4 * kThreads * 16 : 0);
   // set on every call: the attribute belongs to the device that is current
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(kernel, grid, dim3(kThreads), smem, st, d, e);
+  return launch_dependent(kernel, dim3(unsigned(grid)), dim3(kThreads), smem, st, d, e);
 }
 
 cudaError_t launch_expand(const Adapters& d, const Expand& e, int layout, int act, cudaStream_t st, int sms) {
@@ -578,8 +655,9 @@ cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaSt
   if (err != cudaSuccess) return err;
   *launches = 1;
   if (!a.y && !a.h && slices == 1) return cudaSuccess;  // s alone was asked for
-  const Expand e{a.b, true, a.N, a.base, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, slices > 1 ? a.s : nullptr,
-                 0, 0, a.glu_alpha, a.glu_limit};
+  const bool rows = a.y || a.h;  // else only s' parts are to be added
+  const Expand e{a.b, true, a.N, rows ? a.base : nullptr, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, slices > 1 ? a.s : nullptr,
+                 0, a.glu_alpha, a.glu_limit};
   *launches = 2;
   return launch_expand(d, e, a.gate_up_layout, a.activation, st, sms);
 }
@@ -633,7 +711,7 @@ cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flag
       ++*launches;
     }
     if (a.dx) {
-      const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1, nullptr, 0, 0, 0.f, 0.f};
+      const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1, nullptr, 0, 0.f, 0.f};
       if ((err = launch_expand_as<kGluNone, 0, true>(d, e, st, sms)) != cudaSuccess) return err;
       ++*launches;
     }

@@ -39,6 +39,7 @@
 
 #include "common.cuh"
 #include "lora_tc.h"
+#include "lora_walk.cuh"
 #include "sm100.cuh"
 #include "tmap.h"
 
@@ -49,7 +50,7 @@ using namespace sm100;
 
 constexpr int kThreads = 448;
 constexpr int kLoadWarp = 10, kLoadWarps = 4;
-constexpr int kTile = 128;                       // positions, and columns, of a tile
+static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
 constexpr uint32_t kZBytes = 2 * kBox;           // a tile
@@ -95,42 +96,6 @@ __host__ __device__ inline Layout layout_of(const Pass& p, bool out, bool grad) 
   l.total = l.misc + 1024 + 1024;  // barriers and scalars, alignment
   return l;
 }
-
-__host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, int64_t R_max, int64_t& beg, int64_t& end) {
-  beg = offsets[g];
-  end = offsets[g + 1];
-  beg = beg < 0 ? 0 : beg > R_max ? R_max : beg;  // no position outside [0, R_max) is ever formed
-  end = end < 0 ? 0 : end > R_max ? R_max : end;
-  return end > beg ? (end - beg + kTile - 1) / kTile : 0;
-}
-
-// First item of CTA b's run out of W items over n CTAs.
-__host__ __device__ inline int64_t run_start(int64_t W, int64_t n, int64_t b) { return b * W / n; }
-
-// A position in the list of (column block, row tile), row tiles in group order.
-struct Walk {
-  const int64_t* offsets;
-  int64_t R_max, beg, end, tiles;
-  int64_t tile;  // within the group
-  int G, g, cb;
-
-  E4B_DEV void enter(int group) {
-    g = group;
-    tiles = group_tiles(offsets, g, R_max, beg, end);
-  }
-  E4B_DEV void next() {
-    if (++tile < tiles) return;
-    tile = 0;
-    do {
-      if (g + 1 == G) ++cb;
-      enter(g + 1 == G ? 0 : g + 1);
-    } while (tiles == 0);  // some group has rows
-  }
-  E4B_DEV bool first() const { return tile == 0; }
-  E4B_DEV bool last() const { return tile + 1 == tiles; }
-  E4B_DEV int64_t row0() const { return beg + tile * kTile; }
-  E4B_DEV int n() const { return int(end - row0() < kTile ? end - row0() : kTile); }
-};
 
 // Shared-memory descriptors, built once: a step adds its bytes / 16 to the low
 // word (the address field cannot overflow into its neighbour below 256 KB).
@@ -207,8 +172,8 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   uint64_t* v_empty = v_full + 2;
   uint64_t* g_full = v_empty + 2;
   uint64_t* g_empty = g_full + 1;  // [kMaxChunks]
-  int64_t* s_sum = reinterpret_cast<int64_t*>(g_empty + kMaxChunks);  // [kThreads / 32 + 1]
-  int64_t* s_start = s_sum + kThreads / 32 + 1;                       // group, tile
+  int64_t* s_sum = reinterpret_cast<int64_t*>(g_empty + kMaxChunks);  // [kThreads / 32]
+  int64_t* s_start = s_sum + kThreads / 32;                           // group, tile
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_start + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
@@ -216,42 +181,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the row tiles of all groups, and where this CTA's run begins
-  const int per = (p.G + kThreads - 1) / kThreads;
-  const int g_lo = min(tid * per, p.G), g_hi = min(g_lo + per, p.G);
-  int64_t beg, end, mine = 0;
-  for (int g = g_lo; g < g_hi; ++g) mine += group_tiles(p.offsets, g, p.R_max, beg, end);
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, T = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    T += s_sum[w];
-  }
-  const int64_t W = T * p.blocks;
-  const int64_t n_run = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
   if (GRAD && tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
-  if (int64_t(blockIdx.x) >= n_run) return;  // uniform; also where no group has rows
-  const int64_t w0 = run_start(W, n_run, blockIdx.x), w1 = run_start(W, n_run, int64_t(blockIdx.x) + 1);
-  const int64_t rt0 = w0 % T;
-  if (rt0 >= before && rt0 < before + mine) {
-    int64_t left = rt0 - before;
-    for (int g = g_lo; g < g_hi; ++g) {
-      const int64_t t = group_tiles(p.offsets, g, p.R_max, beg, end);
-      if (left < t) {
-        s_start[0] = g;
-        s_start[1] = left;
-        break;
-      }
-      left -= t;
-    }
-  }
+  const Run run = find_run<kThreads>(p.offsets, p.G, p.R_max, p.blocks, s_sum, s_start);
+  if (run.count == 0) return;  // uniform
+  const int64_t count = run.count;
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -279,17 +212,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  const int64_t count = w1 - w0;
   const int all_chunks = int((p.C + kTile - 1) / kTile);
   const int rp = p.rp, gw = p.merged ? 3 * rp : rp;  // TMEM columns of a tile's gradient
   const uint32_t d_grad = tmem + (OUT ? 2 * rp : 0);
-  Walk wk;
-  wk.offsets = p.offsets;
-  wk.R_max = p.R_max;
-  wk.G = p.G;
-  wk.cb = int(w0 / T);
-  wk.enter(int(s_start[0]));
-  wk.tile = s_start[1];
+  Walk wk(p.offsets, p.G, p.R_max, run, s_start);
   auto chunks_of = [&](int cb) { return min(p.chunks, all_chunks - cb * p.chunks); };
   auto give_up = [&]() {
     *s_abort = 1;

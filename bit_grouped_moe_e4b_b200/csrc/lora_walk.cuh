@@ -1,0 +1,105 @@
+// How the adapters' kernels share out their work: the list of (column block, row
+// tile), row tiles of 128 positions in group order, is cut into equal runs for
+// the CTAs, so that the groups' sizes do not unbalance it.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace e4b {
+
+constexpr int kTile = 128;  // positions of a row tile
+
+__host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, int64_t R_max, int64_t& beg, int64_t& end) {
+  beg = offsets[g];
+  end = offsets[g + 1];
+  beg = beg < 0 ? 0 : beg > R_max ? R_max : beg;  // no position outside [0, R_max) is ever formed
+  end = end < 0 ? 0 : end > R_max ? R_max : end;
+  return end > beg ? (end - beg + kTile - 1) / kTile : 0;
+}
+
+// First item of CTA b's run out of W items over n CTAs.
+__host__ __device__ inline int64_t run_start(int64_t W, int64_t n, int64_t b) { return b * W / n; }
+
+// A CTA's run: the column block it begins in, and its items.
+struct Run {
+  int block;
+  int64_t count;
+};
+
+// By the whole CTA (ends with a barrier): the row tiles of all groups are added
+// up, and start receives the group and the tile within it that the run begins
+// with. sums: [THREADS / 32]. count 0: nothing is left for this CTA.
+template <int THREADS>
+E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, int blocks, int64_t* sums, int64_t* start) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int strip = (G + THREADS - 1) / THREADS;
+  const int lo = min(tid * strip, G), hi = min(lo + strip, G);
+  int64_t beg, end, mine = 0;
+  for (int g = lo; g < hi; ++g) mine += group_tiles(offsets, g, R_max, beg, end);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, T = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    T += sums[w];
+  }
+  const int64_t W = T * blocks;
+  const int64_t ctas = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
+  if (int64_t(blockIdx.x) >= ctas) return Run{0, 0};  // uniform; also where no group has rows
+  const int64_t w0 = run_start(W, ctas, blockIdx.x);
+  const int block = int(w0 / T);
+  const int64_t first = w0 - block * T;
+  if (first >= before && first < before + mine) {
+    int64_t left = first - before;
+    for (int g = lo; g < hi; ++g) {
+      const int64_t t = group_tiles(offsets, g, R_max, beg, end);
+      if (left < t) {
+        start[0] = g;
+        start[1] = left;
+        break;
+      }
+      left -= t;
+    }
+  }
+  __syncthreads();
+  return Run{block, run_start(W, ctas, int64_t(blockIdx.x) + 1) - w0};
+}
+
+// A position in the list of (column block, row tile), row tiles in group order.
+struct Walk {
+  const int64_t* offsets;
+  int64_t R_max, beg, end, tiles;
+  int64_t tile;  // within the group
+  int G, g, cb;
+
+  E4B_DEV Walk(const int64_t* offs, int groups, int64_t r_max, const Run& run, const int64_t* start)
+      : offsets(offs), R_max(r_max), tile(start[1]), G(groups), cb(run.block) {
+    enter(int(start[0]));
+  }
+  E4B_DEV void enter(int group) {
+    g = group;
+    tiles = group_tiles(offsets, g, R_max, beg, end);
+  }
+  E4B_DEV void next() {
+    if (++tile < tiles) return;
+    tile = 0;
+    do {
+      if (g + 1 == G) ++cb;
+      enter(g + 1 == G ? 0 : g + 1);
+    } while (tiles == 0);  // some group has rows
+  }
+  E4B_DEV bool first() const { return tile == 0; }
+  E4B_DEV bool last() const { return tile + 1 == tiles; }
+  E4B_DEV int64_t row0() const { return beg + tile * kTile; }
+  E4B_DEV int n() const { return int(end - row0() < kTile ? end - row0() : kTile); }
+};
+
+}  // namespace e4b
