@@ -16,6 +16,10 @@
 // error of 2^-17 a product. The terms lie side by side as columns of one B
 // operand (N = 3 * rank) up to rank 32, and are added when TMEM is read: three
 // MMAs into one accumulator would read the tile from shared memory three times.
+// An MMA truncates its sum, so that n of them in one accumulator are 1.6e-8 n
+// off in the mean (2.1e-6 after 128). Sums therefore leave TMEM after kOutChain
+// column tiles and grad_chain row tiles and go on in fp32 additions: within
+// 1e-6, as products and sums of fp32 are.
 //
 // One persistent CTA per SM. The work is the list of (column block, row tile)
 // in that order, cut into equal runs for the CTAs, so that the groups' sizes do
@@ -54,6 +58,10 @@ static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
 constexpr uint32_t kZBytes = 2 * kBox;           // a tile
+constexpr int kOutChain = 4;                     // tiles of eight MMAs
+// Tiles of eight MMAs, or of 24 (three terms into one accumulator, of which the
+// small ones hardly move the sum).
+__host__ __device__ constexpr int grad_chain(int rp) { return rp <= 32 ? 10 : 6; }
 constexpr int kMaxStages = 6;
 constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
 constexpr uint32_t kSmemLimit = 232448;
@@ -76,11 +84,11 @@ struct Pass {
   float* grad_part;
   Note* notes;  // of the parts, two a CTA
   int32_t* status;
-  int G, r, rp;        // rp: the rank's operand width, 16, 32 or 64
+  int G, r;
   int blocks, chunks;  // column blocks; column tiles of a block
   int stages, vbufs;
   uint32_t limit;
-  uint8_t w_t, scale_out, scale_v, grad_t, accumulate, merged;
+  uint8_t w_t, scale_out, scale_v, grad_t, accumulate;
 };
 
 // Shared memory, from a 1024-byte boundary: stages of (tile, W's box), the
@@ -88,11 +96,11 @@ struct Pass {
 struct Layout {
   uint32_t stage, terms, misc, total;
 };
-__host__ __device__ inline Layout layout_of(const Pass& p, bool out, bool grad) {
+__host__ __device__ inline Layout layout_of(const Pass& p, bool out, bool grad, int rp) {
   Layout l;
-  l.stage = kZBytes + (out ? 2 * kTile * p.rp : 0);
+  l.stage = kZBytes + (out ? 2 * kTile * rp : 0);
   l.terms = l.stage * p.stages;
-  l.misc = l.terms + (grad ? p.vbufs * 6 * kTile * p.rp : 0);
+  l.misc = l.terms + (grad ? p.vbufs * 6 * kTile * rp : 0);
   l.total = l.misc + 1024 + 1024;  // barriers and scalars, alignment
   return l;
 }
@@ -156,13 +164,13 @@ E4B_DEV void split3(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
   lo = make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
 }
 
-template <bool OUT, bool GRAD>
+template <bool OUT, bool GRAD, int RP>  // RP: the rank's operand width, 16, 32 or 64
 __global__ void __launch_bounds__(kThreads, 1)
 contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_constant__ CUtensorMap tm_edge,
                 const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ Pass p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const Layout lay = layout_of(p, OUT, GRAD);
+  const Layout lay = layout_of(p, OUT, GRAD, RP);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.misc);
   uint64_t* loaded = full + kMaxStages;
   uint64_t* empty = loaded + kMaxStages;
@@ -213,7 +221,9 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   const uint32_t tmem = *s_tmem;
 
   const int all_chunks = int((p.C + kTile - 1) / kTile);
-  const int rp = p.rp, gw = p.merged ? 3 * rp : rp;  // TMEM columns of a tile's gradient
+  constexpr int rp = RP;
+  constexpr bool merged = RP <= 32;
+  constexpr int gw = merged ? 3 * rp : rp;  // TMEM columns of a tile's gradient
   const uint32_t d_grad = tmem + (OUT ? 2 * rp : 0);
   Walk wk(p.offsets, p.G, p.R_max, run, s_start);
   auto chunks_of = [&](int cb) { return min(p.chunks, all_chunks - cb * p.chunks); };
@@ -292,21 +302,21 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       uint64_t* last_bar = nullptr;
       uint32_t last_ph = 0;
       bool aborted = false;
-      bool fresh = true;  // first row tile of a gradient
+      bool fresh = true;  // first row tile of a chain
+      int chain = 0;
       for (int64_t k = 0; k < count && !aborted; ++k) {
-        if ((OUT && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort)) ||
-            (GRAD && !mbar_wait_bounded(&v_full[vr.slot], vr.parity, p.limit, s_abort))) {
+        if (GRAD && !mbar_wait_bounded(&v_full[vr.slot], vr.parity, p.limit, s_abort)) {
           give_up();
           break;
         }
         const int steps = (wk.n() + 15) / 16;
         const int nc = chunks_of(wk.cb);
         const uint64_t vd = step_desc(vd0, vr.slot * 6 * kTile * rp);
-        const uint32_t d_out = tmem + tr.slot * rp;
         uint32_t d = d_grad;
         for (int c = 0; c < nc; ++c, d += gw, st.next()) {
           if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
               (loaders && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
+              (OUT && c % kOutChain == 0 && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort)) ||
               (GRAD && fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
             give_up();
             aborted = true;
@@ -318,13 +328,14 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
             const uint64_t zd = step_desc(zk, at), wd = step_desc(wd0, at);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(d_out, step_desc(zd, (kk >> 2) * kBox + (kk & 3) * 32),
-                          step_desc(wd, uint32_t(kk >> 2) * w_half + uint32_t(kk & 3) * w_step), id_out, (c | kk) ? 1u : 0u);
+              mma_bf16_ss(tmem + tr.slot * rp, step_desc(zd, (kk >> 2) * kBox + (kk & 3) * 32),
+                          step_desc(wd, uint32_t(kk >> 2) * w_half + uint32_t(kk & 3) * w_step), id_out,
+                          (c % kOutChain | kk) ? 1u : 0u);
           }
           if (GRAD) {
             if (fresh) g_phase ^= 1u << c;
             const uint64_t zd = step_desc(zm, at);
-            if (p.merged) {
+            if constexpr (merged) {
               uint64_t vs = vd;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
@@ -347,15 +358,18 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           mma_commit(&empty[st.slot]);
           last_bar = &empty[st.slot];
           last_ph = st.parity;
+          if (OUT && (c % kOutChain == kOutChain - 1 || c + 1 == nc)) {
+            mma_commit(&t_full[tr.slot]);
+            tr.next();
+          }
         }
         if (aborted) break;
-        if (OUT) mma_commit(&t_full[tr.slot]);
         if (GRAD) {
           mma_commit(&v_empty[vr.slot]);
-          fresh = wk.last();
+          fresh = ++chain == grad_chain(RP) || wk.last();
           if (fresh || k + 1 == count) mma_commit(g_full);
+          if (fresh) chain = 0;
         }
-        tr.next();
         vr.next();
         if (k + 1 < count) wk.next();
       }
@@ -376,9 +390,9 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           in = at >= 0 && at < p.rows;
         }
         const float w = p.scale_v && p.scale ? __ldg(p.scale + wk.g) : 1.f;
-        float4 x[16];
+        float4 x[RP / 4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < RP / 4; ++j)
           x[j] = in && 4 * j < p.r ? __ldg(reinterpret_cast<const float4*>(p.v + pos * p.r) + j)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
         if (!warp_wait(&v_empty[vr.slot], vr.parity ^ 1u, p.limit, s_abort)) {
@@ -386,8 +400,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           break;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (8 * j >= rp) break;
+        for (int j = 0; j < RP / 8; ++j) {
           const float f[8] = {w * x[2 * j].x, w * x[2 * j].y, w * x[2 * j].z, w * x[2 * j].w,
                               w * x[2 * j + 1].x, w * x[2 * j + 1].y, w * x[2 * j + 1].z, w * x[2 * j + 1].w};
           uint4 hi, mid, lo;
@@ -494,50 +507,62 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     const int q = warp & 3;  // the TMEM lanes this warp may read
     const int m = q * 32 + lane;
     const uint32_t lanes = uint32_t(q * 32) << 16;
-    int64_t seg0 = 0;  // first item of the gradient's row tiles in this run
-    uint32_t segs = 0;
-    bool whole_start = wk.first();
     Ring tr(2);
-    for (int64_t k = 0; k < count; ++k, tr.next()) {
+    uint32_t chains = 0;
+    int chain = 0;
+    bool direct = false, later = false;  // the gradient goes to its place; it is there in part
+    int part = 0;
+    for (int64_t k = 0; k < count; ++k) {
       if constexpr (OUT) {
-        if (!warp_wait(&t_full[tr.slot], tr.parity, p.limit, s_abort)) {
+        float sum[RP];
+        const int nc = chunks_of(wk.cb);
+        bool ok = true;
+        for (int c = 0; c < nc; c += kOutChain, tr.next()) {
+          ok = warp_wait(&t_full[tr.slot], tr.parity, p.limit, s_abort);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j0 = 0; j0 < RP; j0 += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tmem + lanes + tr.slot * rp + j0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[j0 + j] = c ? sum[j0 + j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+          }
+          tc_fence_before();
+          mbar_arrive(&t_empty[tr.slot]);
+        }
+        if (!ok) {
           give_up();
           break;
         }
-        tc_fence_after();
-        const bool in = m < wk.n();
         const float w = p.scale_out && p.scale ? __ldg(p.scale + wk.g) : 1.f;
         float* dst = p.out + (int64_t(wk.cb) * p.R_max + wk.row0() + m) * p.r;
-        for (int j0 = 0; j0 < rp; j0 += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tmem + lanes + tr.slot * rp + j0, v);
-          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            if (in && j0 + j < p.r)
-              *reinterpret_cast<float4*>(dst + j0 + j) =
-                  make_float4(w * __uint_as_float(v[j]), w * __uint_as_float(v[j + 1]), w * __uint_as_float(v[j + 2]),
-                              w * __uint_as_float(v[j + 3]));
-        }
-        tc_fence_before();
-        mbar_arrive(&t_empty[tr.slot]);
+        for (int j = 0; j < RP; j += 4)
+          if (m < wk.n() && j < p.r)
+            *reinterpret_cast<float4*>(dst + j) = make_float4(w * sum[j], w * sum[j + 1], w * sum[j + 2], w * sum[j + 3]);
       }
       if constexpr (GRAD) {
-        const bool done = wk.last();
-        if (done || k + 1 == count) {
-          if (!warp_wait(g_full, segs & 1u, p.limit, s_abort)) {
+        if (k == 0 || wk.first()) {  // the next gradient of this run
+          direct = wk.first() && wk.tiles <= count - k;
+          later = false;
+          part = 2 * int(blockIdx.x) + (k ? 1 : 0);
+          if (!direct && m == 0) p.notes[part] = Note{wk.g, wk.cb, wk.first()};
+        }
+        const bool fresh = ++chain == grad_chain(RP) || wk.last();
+        if (fresh || k + 1 == count) {
+          chain = 0;
+          if (!warp_wait(g_full, chains++ & 1u, p.limit, s_abort)) {
             give_up();
             break;
           }
           tc_fence_after();
-          const bool direct = whole_start && done;
           const int64_t block = int64_t(p.chunks) * kTile;  // columns of a part
           const int64_t col0 = direct ? wk.cb * block : 0, width = direct ? p.C : block;
-          float* dst = direct ? p.grad + int64_t(wk.g) * p.C * p.r
-                              : p.grad_part + (2 * int64_t(blockIdx.x) + (seg0 == 0 ? 0 : 1)) * block * p.r;
-          const bool add = direct && p.accumulate;
-          if (!direct && m == 0)
-            p.notes[2 * blockIdx.x + (seg0 == 0 ? 0 : 1)] = Note{wk.g, wk.cb, whole_start};
+          float* dst = direct ? p.grad + int64_t(wk.g) * p.C * p.r : p.grad_part + part * block * p.r;
+          const bool add = later || (direct && p.accumulate);
+          later = true;
           const int nc = chunks_of(wk.cb);
           for (int c = 0; c < nc; ++c) {
             const int64_t n = int64_t(c) * kTile + m;
@@ -547,7 +572,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
               uint32_t v[16];
               const uint32_t at = d_grad + lanes + uint32_t(c * gw + j0);
               tmem_ld_32x32b_x16(at, v);
-              if (p.merged) {
+              if constexpr (merged) {
                 uint32_t v1[16], v2[16];
                 tmem_ld_32x32b_x16(at + rp, v1);
                 tmem_ld_32x32b_x16(at + 2 * rp, v2);
@@ -587,9 +612,6 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
               }
             }
           }
-          ++segs;
-          seg0 = k + 1;
-          whole_start = true;  // the next one begins with its group
         }
       }
       if (k + 1 < count) wk.next();
@@ -672,7 +694,7 @@ finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b
 
 // ---------------------------------------------------------------- the plan
 struct Plan {
-  int rp, merged, chunks, blocks, vbufs, stages;
+  int rp, chunks, blocks, vbufs, stages;
 };
 
 // Column tiles of a block: at most those whose gradients TMEM holds, and of
@@ -684,8 +706,7 @@ struct Plan {
 Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
   Plan q;
   q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
-  q.merged = q.rp <= 32;
-  const int gw = q.merged ? 3 * q.rp : q.rp;
+  const int gw = q.rp <= 32 ? 3 * q.rp : q.rp;
   int most = grad ? (512 - (out ? 2 * q.rp : 0)) / gw : 64;
   if (grad && most > kMaxChunks) most = kMaxChunks;
   const int64_t all = (C + kTile - 1) / kTile;
@@ -733,7 +754,6 @@ Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   p.status = a.status;
   p.G = a.G;
   p.r = a.r;
-  p.rp = q.rp;
   p.blocks = q.blocks;
   p.chunks = q.chunks;
   p.stages = q.stages;
@@ -744,18 +764,25 @@ Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   p.scale_v = a.scale_v;
   p.grad_t = a.grad_t;
   p.accumulate = a.accumulate;
-  p.merged = q.merged;
   return p;
 }
 
-template <bool OUT, bool GRAD>
+template <bool OUT, bool GRAD, int RP>
 cudaError_t launch(const CUtensorMap& tile, const CUtensorMap& edge, const CUtensorMap& w, const Pass& p, cudaStream_t st, int sms) {
-  auto kernel = contract_kernel<OUT, GRAD>;
-  const uint32_t smem = layout_of(p, OUT, GRAD).total;
+  auto kernel = contract_kernel<OUT, GRAD, RP>;
+  const uint32_t smem = layout_of(p, OUT, GRAD, RP).total;
   // set on every call: the attribute belongs to the device that is current
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, dim3(sms), dim3(kThreads), smem, st, tile, edge, w, p);
+}
+
+template <int RP>
+cudaError_t launch_as(const ContractArgs& a, const CUtensorMap& tile, const CUtensorMap& edge, const CUtensorMap& w,
+                      const Pass& p, cudaStream_t st, int sms) {
+  if (!a.grad) return launch<true, false, RP>(tile, edge, w, p, st, sms);
+  if (!a.out) return launch<false, true, RP>(tile, edge, w, p, st, sms);
+  return launch<true, true, RP>(tile, edge, w, p, st, sms);
 }
 
 }  // namespace
@@ -788,9 +815,9 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
     w = tile;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (!a.grad) return launch<true, false>(tile, edge, w, p, st, sms);
-  if (!a.out) return launch<false, true>(tile, edge, w, p, st, sms);
-  return launch<true, true>(tile, edge, w, p, st, sms);
+  if (q.rp == 16) return launch_as<16>(a, tile, edge, w, p, st, sms);
+  if (q.rp == 32) return launch_as<32>(a, tile, edge, w, p, st, sms);
+  return launch_as<64>(a, tile, edge, w, p, st, sms);
 }
 
 cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
