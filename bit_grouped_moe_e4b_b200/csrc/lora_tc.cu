@@ -16,10 +16,10 @@
 // error of 2^-17 a product. The terms lie side by side as columns of one B
 // operand (N = 3 * rank) up to rank 32, and are added when TMEM is read: three
 // MMAs into one accumulator would read the tile from shared memory three times.
-// An MMA truncates its sum, so that n of them in one accumulator are 1.6e-8 n
-// off in the mean (2.1e-6 after 128). Sums therefore leave TMEM after kOutChain
-// column tiles and grad_chain row tiles and go on in fp32 additions: within
-// 1e-6, as products and sums of fp32 are.
+// An MMA truncates its sum, so that n of them in one accumulator leave it 1.2e-8
+// n too small (2.1e-6 after 128, measured), and dA inherits t's share. Sums
+// therefore leave TMEM after kOutChain column tiles and grad_chain row tiles and
+// go on in fp32 additions: within 1e-6, as products and sums of fp32 are.
 //
 // One persistent CTA per SM. The work is the list of (column block, row tile)
 // in that order, cut into equal runs for the CTAs, so that the groups' sizes do
@@ -58,10 +58,10 @@ static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
 constexpr uint32_t kZBytes = 2 * kBox;           // a tile
-constexpr int kOutChain = 4;                     // tiles of eight MMAs
+constexpr int kOutChain = 2;                     // tiles of eight MMAs
 // Tiles of eight MMAs, or of 24 (three terms into one accumulator, of which the
 // small ones hardly move the sum).
-__host__ __device__ constexpr int grad_chain(int rp) { return rp <= 32 ? 10 : 6; }
+__host__ __device__ constexpr int grad_chain(int rp) { return rp <= 32 ? 8 : 2; }
 constexpr int kMaxStages = 6;
 constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
 constexpr uint32_t kSmemLimit = 232448;
@@ -563,19 +563,41 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           float* dst = direct ? p.grad + int64_t(wk.g) * p.C * p.r : p.grad_part + part * block * p.r;
           const bool add = later || (direct && p.accumulate);
           later = true;
+          // this thread's column of chunk c: its rank's values lie `step` apart
           const int nc = chunks_of(wk.cb);
+          const int64_t left = p.C - wk.cb * block - m;  // chunk c is within the columns where 128 c < left
+          float* at = dst + (p.grad_t ? (col0 + m) * p.r : col0 + m);
+          const int64_t chunk_step = p.grad_t ? int64_t(kTile) * p.r : kTile;
+          float old[16];  // what the next values are added to
+          auto fetch_old = [&](int c, int j0) {
+            const float* o = at + c * chunk_step;
+            const bool in = add && c < nc && c * kTile < left;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              if (p.grad_t) {
+                const float4 v = in && j0 + j < p.r ? *reinterpret_cast<const float4*>(o + j0 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                old[j] = v.x;
+                old[j + 1] = v.y;
+                old[j + 2] = v.z;
+                old[j + 3] = v.w;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) old[j + i] = in && j0 + j < p.r ? o[(j0 + j + i) * width] : 0.f;
+              }
+            }
+          };
+          if (add) fetch_old(0, 0);
           for (int c = 0; c < nc; ++c) {
-            const int64_t n = int64_t(c) * kTile + m;
-            const bool in = wk.cb * block + n < p.C;
-            for (int j0 = 0; j0 < rp; j0 += 16) {
+#pragma unroll
+            for (int j0 = 0; j0 < RP; j0 += 16) {
               float f[16];
               uint32_t v[16];
-              const uint32_t at = d_grad + lanes + uint32_t(c * gw + j0);
-              tmem_ld_32x32b_x16(at, v);
+              const uint32_t from = d_grad + lanes + uint32_t(c * gw + j0);
+              tmem_ld_32x32b_x16(from, v);
               if constexpr (merged) {
                 uint32_t v1[16], v2[16];
-                tmem_ld_32x32b_x16(at + rp, v1);
-                tmem_ld_32x32b_x16(at + 2 * rp, v2);
+                tmem_ld_32x32b_x16(from + rp, v1);
+                tmem_ld_32x32b_x16(from + 2 * rp, v2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -585,29 +607,26 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
               }
-              if (j0 + 16 >= rp) {
+              if (j0 + 16 >= RP) {
                 tc_fence_before();
                 mbar_arrive(&g_empty[c]);
               }
-              if (!in) continue;
-              if (p.grad_t) {
-                float4* at4 = reinterpret_cast<float4*>(dst + (col0 + n) * p.r + j0);
+              if (add) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  if (j0 + 4 * j >= p.r) break;
-                  float4 o = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-                  if (add) {
-                    const float4 w = at4[j];
-                    o = make_float4(w.x + o.x, w.y + o.y, w.z + o.z, w.w + o.w);
-                  }
-                  at4[j] = o;
-                }
-              } else {
+                for (int j = 0; j < 16; ++j) f[j] += old[j];
+                if (j0 + 16 < RP) fetch_old(c, j0 + 16);
+                else fetch_old(c + 1, 0);
+              }
+              if (c * kTile >= left) continue;
+              float* o = at + c * chunk_step;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  if (j0 + j >= p.r) break;
-                  float* at1 = dst + int64_t(j0 + j) * width + col0 + n;
-                  *at1 = add ? *at1 + f[j] : f[j];
+              for (int j = 0; j < 16; j += 4) {
+                if (j0 + j >= p.r) break;
+                if (p.grad_t) {
+                  *reinterpret_cast<float4*>(o + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[(j0 + j + i) * width] = f[j + i];
                 }
               }
             }
