@@ -652,36 +652,54 @@ struct Finish {
 };
 
 // The parts that begin in CTA b of the pass: each goes on in the first parts of
-// the CTAs after it.
+// the CTAs after it. kFinishVecs vectors a thread, in flight together.
+constexpr int kFinishVecs = 4;
 E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
   const Pass& p = f.p;
+  __shared__ int s_last;
   const int64_t block = int64_t(p.chunks) * kTile, part = block * p.r;
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const Note note = p.notes[2 * b + k];
-    if (note.group < 0 || !note.first) continue;
-    int last = b;
-    while (last + 1 < f.ctas) {
-      const Note more = p.notes[2 * (last + 1)];
-      if (more.group != note.group || more.block != note.block || more.first) break;
-      ++last;
+    if (note.group < 0 || !note.first) continue;  // uniform
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = f.ctas - 1;
+    __syncthreads();
+    for (int c = b + 1 + threadIdx.x; c < f.ctas; c += 256) {  // the first CTA that does not go on with it
+      const Note more = p.notes[2 * c];
+      if (more.group != note.group || more.block != note.block || more.first) atomicMin(&s_last, c - 1);
     }
+    __syncthreads();
+    const int last = s_last;
     const int64_t c0 = note.block * block;
     const int cols = int(min(block, p.C - c0));
     // values that lie together: the block's columns by r, or r rows of its columns
     const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
     float* dst = p.grad + int64_t(note.group) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
-    for (int i = piece * 256 + int(threadIdx.x); i < lines * len4; i += 256 * int(gridDim.y)) {
-      const int line = i / len4, at = (i - line * len4) * 4;
-      float4* out = reinterpret_cast<float4*>(dst + line * p.C + at);
-      float4 s = p.accumulate ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float* src = p.grad_part + line * block + at;
+    const int total = lines * len4, step = 256 * int(gridDim.y);
+    for (int i0 = piece * 256 + int(threadIdx.x); i0 < total; i0 += kFinishVecs * step) {
+      float4 s[kFinishVecs];
+      int64_t src[kFinishVecs], to[kFinishVecs];
+#pragma unroll
+      for (int v = 0; v < kFinishVecs; ++v) {
+        const int i = i0 + v * step, line = i / len4, at = (i - line * len4) * 4;
+        to[v] = i < total ? line * p.C + at : -1;
+        src[v] = line * block + at;
+        s[v] = p.accumulate && to[v] >= 0 ? *reinterpret_cast<const float4*>(dst + to[v]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll 2
       for (int c = b; c <= last; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (2 * c + (c == b ? k : 0)) * part);
-        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        const float* from = p.grad_part + (2 * c + (c == b ? k : 0)) * part;
+#pragma unroll
+        for (int v = 0; v < kFinishVecs; ++v) {
+          if (to[v] < 0) continue;
+          const float4 z = __ldg(reinterpret_cast<const float4*>(from + src[v]));
+          s[v] = make_float4(s[v].x + z.x, s[v].y + z.y, s[v].z + z.z, s[v].w + z.w);
+        }
       }
-      *out = s;
+#pragma unroll
+      for (int v = 0; v < kFinishVecs; ++v)
+        if (to[v] >= 0) *reinterpret_cast<float4*>(dst + to[v]) = s[v];
     }
   }
 }
@@ -850,8 +868,8 @@ cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b,
     if (most < f[i].p.chunks) most = f[i].p.chunks;
     ++i;
   }
-  // a part's values over CTAs, four a thread
-  const int pieces = (most * kTile * a->r + 4095) / 4096;
+  const int per = 256 * kFinishVecs * 4;  // a part's values over CTAs
+  const int pieces = (most * kTile * a->r + per - 1) / per;
   return launch_dependent(finish_kernel, dim3(unsigned(ctas), unsigned(pieces)), dim3(256), 0, st, f[0], f[1]);
 }
 
