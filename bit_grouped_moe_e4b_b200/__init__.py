@@ -6,4 +6,4 @@ does not load the library; the first call into ``e4b`` does, and raises if the
 library is missing. There is no CPU fallback.
 """
 
-__all__ = ["configs", "synth", "e4b"]
+__all__ = ["configs", "synth", "e4b", "qlora"]

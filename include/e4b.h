@@ -589,8 +589,8 @@ e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
  * all pointers but offsets, row and scale 16-byte aligned. ws: device scratch of
  * e4b_lora_workspace_size bytes (16-byte aligned), for one call at a time.
  * flags: E4B_FLAG_ACCUMULATE (backward), E4B_FLAG_TEST_TIMEOUT. A wait on the GPU
- * that gives up records E4B_ERR_DEVICE_TIMEOUT in *status (the caller zeroes it)
- * and leaves results unwritten.
+ * that gives up records E4B_ERR_DEVICE_TIMEOUT in *status (the caller zeroes it);
+ * the results are then undefined.
  * Launches: 2 forward, up to 5 backward.
  */
 #define E4B_FLAG_ACCUMULATE 0x100u /* e4b_lora_backward: add to da and db */
