@@ -219,6 +219,7 @@ struct Expand {
   int64_t ld_h;
   const float* v;  // [slices][R_max][r]
   int slices;
+  bool beside;     // nothing comes from the launch before this one but its own earlier work
   float* v_out;    // the slices' sum, written by the first columns' CTAs; or null
   int col_blocks;
   float alpha, limit;
@@ -264,16 +265,24 @@ E4B_DEV float4 sum_slices(const Adapters& d, const Expand& e, int32_t p, int j) 
 }
 
 // KS: MMA k-steps over the rank (r <= 16 KS); ACT: the activation behind GLU.
+// W's fragments take 8 KS registers a strip: above rank 32 a warp has one strip
+// where the activation does not need two, so that two CTAs fit an SM.
+template <int KS, int GLU>
+constexpr int kStrips = KS > 2 && GLU == kGluNone ? 1 : 2;
+template <int KS, int GLU>
+constexpr int kExpandCtas = KS > 2 && kStrips<KS, GLU> == 2 ? 1 : 2;
+
 template <int KS, int GLU, int ACT, bool WT>
-__global__ void __launch_bounds__(kThreads, KS > 2 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, kExpandCtas<KS, GLU>)
 expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand e) {
+  constexpr int ST = kStrips<KS, GLU>;
   struct Item {
     int32_t g, cb, row0, n;
   };
   extern __shared__ uint4 smem[];
   using Frags = uint4[kSixteens][KS][2][32];
   Frags* frags = reinterpret_cast<Frags*>(smem);                 // [2]
-  uint4* ring = smem + 2 * sizeof(Frags) / sizeof(uint4);        // [kAhead + 1][2][2][kThreads], with base
+  uint4* ring = smem + 2 * sizeof(Frags) / sizeof(uint4);        // [kAhead + 1][2][ST][kThreads], with base
   __shared__ int32_t at[2][kTile];
   __shared__ Item items[3];
   __shared__ int64_t s_sum[kWarps], s_start[2];
@@ -283,7 +292,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   const int64_t limit[2] = {GLU == kGluHalves ? half : e.C, e.C};
   // first columns of the warp's strips
   auto strip = [&](int cb, int st) {
-    const int64_t c = (int64_t(cb) * kWarps + warp) * (GLU == kGluHalves ? 32 : 64);
+    const int64_t c = (int64_t(cb) * kWarps + warp) * (GLU == kGluHalves ? 32 : 32 * ST);
     return GLU == kGluHalves ? st * half + c : c + 32 * st;
   };
 
@@ -303,11 +312,11 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   }
   __syncthreads();
 
-  uint32_t bf[2][4][KS][2];
+  uint32_t bf[ST][4][KS][2];
   auto load_w = [&](const Item& t) {
     const uint16_t* wg = e.w + int64_t(t.g) * e.C * d.r;
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
+    for (int st = 0; st < ST; ++st) {
       if constexpr (WT) {
         const int64_t n = strip(t.cb, st) + 8 * (rr >> 1);
 #pragma unroll
@@ -379,24 +388,25 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   };
 
   // W does not come from the launch before this one, which has itself waited
-  // for all earlier work
+  // for all earlier work; nor does anything where it is `beside`, and the wait
+  // comes at the end, for the launch after this one
   Item t = items[0];
   load_w(t);
-  grid_dependency_wait();
+  if (!e.beside) grid_dependency_wait();
   grid_launch_dependents();
   load_v(t);
   store_v(0);
   __syncthreads();
 
   int asked = 0, taken = 0;  // sixteens of base: asked for, and used
-  auto slot = [&](int k, int i, int st) { return ring + ((k % (kAhead + 1) * 2 + i) * 2 + st) * kThreads + tid; };
+  auto slot = [&](int k, int i, int st) { return ring + ((k % (kAhead + 1) * 2 + i) * ST + st) * kThreads + tid; };
   auto fetch = [&](int buf, int six, int cb) {
     if (e.base) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int32_t row = at[buf][16 * six + rr + 8 * i];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+        for (int st = 0; st < ST; ++st) {
           const int64_t c = strip(cb, st) + 8 * q;
           if (row >= 0 && c < limit[st]) sm100::cp_async_16(slot(asked, i, st), e.base + int64_t(row) * e.ld_base + c, 16);
         }
@@ -426,8 +436,13 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
     const int stage_at = sixteens > kAhead ? sixteens - kAhead : 0;  // from here on the next item's rows are asked for
     int next_had = 0;
     while (had < sixteens && had < kAhead) fetch(buf, had++, t.cb);
-    const int64_t c[2] = {strip(t.cb, 0) + 8 * q, strip(t.cb, 1) + 8 * q};
-    const bool in[2] = {c[0] < limit[0], c[1] < limit[1]};
+    int64_t c[ST];
+    bool in[ST];
+#pragma unroll
+    for (int st = 0; st < ST; ++st) {
+      c[st] = strip(t.cb, st) + 8 * q;
+      in[st] = c[st] < limit[st];
+    }
     for (int six = 0; six < sixteens; ++six) {
       if (more && six == stage_at) {
         __syncthreads();  // all warps are past the item that used these fragments
@@ -441,12 +456,12 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
         fetch(buf ^ 1, next_had++, next.cb);
       arrived();
       int32_t row[2];
-      float acc[2][4][4];  // starts as base
+      float acc[ST][4][4];  // starts as base
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         row[i] = at[buf][16 * six + rr + 8 * i];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+        for (int st = 0; st < ST; ++st) {
           const uint4 b = e.base && in[st] && row[i] >= 0 ? *slot(taken, i, st) : make_uint4(0, 0, 0, 0);
           const uint32_t words[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -464,16 +479,16 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
         for (int part = 0; part < 2; ++part) {
           const uint4 f = frags[buf][six][ks][part][lane];
 #pragma unroll
-          for (int st = 0; st < 2; ++st)
+          for (int st = 0; st < ST; ++st)
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_bf16(acc[st][i], f.x, f.y, f.z, f.w, bf[st][i][ks][0], bf[st][i][ks][1]);
         }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (row[i] < 0) continue;
-        float v[2][8];
+        float v[ST][8];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+        for (int st = 0; st < ST; ++st) {
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             v[st][2 * p] = acc[st][p][2 * i];
@@ -488,7 +503,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
           if (in[0]) *reinterpret_cast<uint4*>(e.h + int64_t(row[i]) * e.ld_h + c[0]) = pack8(h);
         } else if constexpr (GLU == kGluInterleaved) {
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
+          for (int st = 0; st < ST; ++st) {
             float h[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p) h[p] = activate<ACT>(v[st][2 * p], v[st][2 * p + 1], e.alpha, e.limit);
@@ -503,6 +518,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
     t = next;
     had = next_had;
   }
+  if (e.beside) grid_dependency_wait();
 }
 
 // The parts' sum: eight threads a float4 take every eighth part, and their
@@ -575,19 +591,26 @@ int forward_slices(int G, int r, int64_t K, int64_t R_max, int sms) {
   return int(want < 1 ? 1 : want);
 }
 
-template <int GLU, int ACT, bool WT>
-cudaError_t launch_expand_as(const Adapters& d, Expand e, cudaStream_t st, int sms) {
-  const int64_t cols = GLU == kGluHalves ? e.C / 2 : e.C, per = kWarps * (GLU == kGluHalves ? 32 : 64);
-  const int KS = d.r <= 16 ? 1 : d.r <= 32 ? 2 : 4;
+template <int KS, int GLU, int ACT, bool WT>
+cudaError_t launch_expand_of(const Adapters& d, Expand e, cudaStream_t st, int sms) {
+  constexpr int strips = kStrips<KS, GLU>;
+  const int64_t cols = GLU == kGluHalves ? e.C / 2 : e.C, per = kWarps * (GLU == kGluHalves ? 32 : 32 * strips);
   e.col_blocks = int((cols + per - 1) / per);
   int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, kTile);
-  if (grid > int64_t(sms) * (KS > 2 ? 1 : 2)) grid = int64_t(sms) * (KS > 2 ? 1 : 2);
-  auto kernel = KS == 1 ? expand_kernel<1, GLU, ACT, WT> : KS == 2 ? expand_kernel<2, GLU, ACT, WT> : expand_kernel<4, GLU, ACT, WT>;
-  const int smem = 2 * kSixteens * KS * 64 * 16 + (e.base ? (kAhead + 1) * 4 * kThreads * 16 : 0);
+  if (grid > int64_t(sms) * kExpandCtas<KS, GLU>) grid = int64_t(sms) * kExpandCtas<KS, GLU>;
+  auto kernel = expand_kernel<KS, GLU, ACT, WT>;
+  const int smem = 2 * kSixteens * KS * 64 * 16 + (e.base ? (kAhead + 1) * 2 * strips * kThreads * 16 : 0);
   // set on every call: the attribute belongs to the device that is current
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, dim3(unsigned(grid)), dim3(kThreads), smem, st, d, e);
+}
+
+template <int GLU, int ACT, bool WT>
+cudaError_t launch_expand_as(const Adapters& d, const Expand& e, cudaStream_t st, int sms) {
+  if (d.r <= 16) return launch_expand_of<1, GLU, ACT, WT>(d, e, st, sms);
+  if (d.r <= 32) return launch_expand_of<2, GLU, ACT, WT>(d, e, st, sms);
+  return launch_expand_of<4, GLU, ACT, WT>(d, e, st, sms);
 }
 
 cudaError_t launch_expand(const Adapters& d, const Expand& e, int layout, int act, cudaStream_t st, int sms) {
@@ -656,8 +679,8 @@ cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaSt
   *launches = 1;
   if (!a.y && !a.h && slices == 1) return cudaSuccess;  // s alone was asked for
   const bool rows = a.y || a.h;  // else only s' parts are to be added
-  const Expand e{a.b, true, a.N, rows ? a.base : nullptr, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, slices > 1 ? a.s : nullptr,
-                 0, a.glu_alpha, a.glu_limit};
+  const Expand e{a.b, true, a.N, rows ? a.base : nullptr, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, false,
+                 slices > 1 ? a.s : nullptr, 0, a.glu_alpha, a.glu_limit};
   *launches = 2;
   return launch_expand(d, e, a.gate_up_layout, a.activation, st, sms);
 }
@@ -711,7 +734,8 @@ cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flag
       ++*launches;
     }
     if (a.dx) {
-      const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1, nullptr, 0, 0.f, 0.f};
+      const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1,
+                     a.da != nullptr, nullptr, 0, 0.f, 0.f};  // da's pass has waited for t and does not write it
       if ((err = launch_expand_as<kGluNone, 0, true>(d, e, st, sms)) != cudaSuccess) return err;
       ++*launches;
     }

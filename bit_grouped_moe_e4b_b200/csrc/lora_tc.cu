@@ -653,8 +653,8 @@ struct Finish {
 
 // The parts that begin in CTA b of the pass: each goes on in the first parts of
 // the CTAs after it. kFinishVecs vectors a thread, in flight together.
-constexpr int kFinishVecs = 4;
-E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
+constexpr int kFinishThreads = 256, kFinishVecs = 4;
+E4B_DEV void finish_parts(const Finish& f, int b) {
   const Pass& p = f.p;
   __shared__ int s_last;
   const int64_t block = int64_t(p.chunks) * kTile, part = block * p.r;
@@ -665,7 +665,7 @@ E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
     __syncthreads();
     if (threadIdx.x == 0) s_last = f.ctas - 1;
     __syncthreads();
-    for (int c = b + 1 + threadIdx.x; c < f.ctas; c += 256) {  // the first CTA that does not go on with it
+    for (int c = b + 1 + threadIdx.x; c < f.ctas; c += kFinishThreads) {  // the first CTA that does not go on with it
       const Note more = p.notes[2 * c];
       if (more.group != note.group || more.block != note.block || more.first) atomicMin(&s_last, c - 1);
     }
@@ -676,8 +676,8 @@ E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
     // values that lie together: the block's columns by r, or r rows of its columns
     const int len4 = (p.grad_t ? cols * p.r : cols) / 4, lines = p.grad_t ? 1 : p.r;
     float* dst = p.grad + int64_t(note.group) * p.C * p.r + (p.grad_t ? c0 * p.r : c0);
-    const int total = lines * len4, step = 256 * int(gridDim.y);
-    for (int i0 = piece * 256 + int(threadIdx.x); i0 < total; i0 += kFinishVecs * step) {
+    const int total = lines * len4, step = kFinishThreads * int(gridDim.y);
+    for (int i0 = int(blockIdx.y) * kFinishThreads + int(threadIdx.x); i0 < total; i0 += kFinishVecs * step) {
       float4 s[kFinishVecs];
       int64_t src[kFinishVecs], to[kFinishVecs];
 #pragma unroll
@@ -704,28 +704,40 @@ E4B_DEV void finish_parts(const Finish& f, int b, int piece) {
   }
 }
 
-E4B_DEV void finish_empty(const Finish& f, int g, int piece) {
-  const Pass& p = f.p;
-  int64_t beg, end;
-  if (p.accumulate || group_tiles(p.offsets, g, p.R_max, beg, end)) return;
+// This CTA's share of the gradients of group g, which has no rows.
+E4B_DEV void finish_empty(const Pass& p, int g) {
   const int64_t n4 = p.C * p.r / 4;
   float4* dst = reinterpret_cast<float4*>(p.grad) + int64_t(g) * n4;
-  for (int64_t i = piece * 256 + threadIdx.x; i < n4; i += 256 * gridDim.y) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t cta = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, ctas = int64_t(gridDim.x) * gridDim.y;
+  for (int64_t i = cta * kFinishThreads + threadIdx.x; i < n4; i += ctas * kFinishThreads)
+    dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// CTAs (x, y): of the first pass' parts, of the second's, of the groups.
-__global__ void __launch_bounds__(256)
+// CTAs (x, y): piece y of the first pass' parts, then of the second's; all of them
+// share the groups without rows.
+__global__ void __launch_bounds__(kFinishThreads)
 finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int x = blockIdx.x;
-  if (x < a.ctas) {
-    finish_parts(a, x, blockIdx.y);
-  } else if (x < a.ctas + b.ctas) {
-    finish_parts(b, x - a.ctas, blockIdx.y);
-  } else {
-    finish_empty(a, x - a.ctas - b.ctas, blockIdx.y);
-    if (b.p.grad) finish_empty(b, x - a.ctas - b.ctas, blockIdx.y);
+  if (x < a.ctas) finish_parts(a, x);
+  else if (x < a.ctas + b.ctas) finish_parts(b, x - a.ctas);
+  if (a.p.accumulate) return;
+  const Pass& p = a.p;
+  __shared__ uint32_t s_empty[kFinishThreads / 32];
+  for (int g0 = 0; g0 < p.G; g0 += kFinishThreads) {
+    const int g = g0 + int(threadIdx.x);
+    int64_t beg, end;
+    const uint32_t empty = __ballot_sync(0xffffffffu, g < p.G && group_tiles(p.offsets, g, p.R_max, beg, end) == 0);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_empty[threadIdx.x >> 5] = empty;
+    __syncthreads();
+    for (int w = 0; w < kFinishThreads / 32; ++w)
+      for (uint32_t left = s_empty[w]; left; left &= left - 1) {
+        const int k = g0 + 32 * w + __ffs(left) - 1;
+        finish_empty(a.p, k);
+        if (b.p.grad) finish_empty(b.p, k);
+      }
   }
 }
 
@@ -859,7 +871,7 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
 
 cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b, cudaStream_t st, int sms) {
   Finish f[2] = {};
-  int ctas = a->G, i = 0, most = 0;
+  int ctas = 0, i = 0, most = 0;
   for (const ContractArgs* c : {a, b}) {
     if (!c) continue;
     f[i].p = pass_of(*c, plan_of(c->G, c->r, c->C, c->R_max, c->out != nullptr, true, sms), sms);
@@ -868,9 +880,9 @@ cudaError_t launch_contract_finish(const ContractArgs* a, const ContractArgs* b,
     if (most < f[i].p.chunks) most = f[i].p.chunks;
     ++i;
   }
-  const int per = 256 * kFinishVecs * 4;  // a part's values over CTAs
-  const int pieces = (most * kTile * a->r + per - 1) / per;
-  return launch_dependent(finish_kernel, dim3(unsigned(ctas), unsigned(pieces)), dim3(256), 0, st, f[0], f[1]);
+  if (!ctas) ctas = 2 * sms;
+  const int per = kFinishThreads * kFinishVecs * 4, pieces = (most * kTile * a->r + per - 1) / per;
+  return launch_dependent(finish_kernel, dim3(unsigned(ctas), unsigned(pieces)), dim3(kFinishThreads), 0, st, f[0], f[1]);
 }
 
 }  // namespace e4b
