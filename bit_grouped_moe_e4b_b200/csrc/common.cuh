@@ -1,6 +1,7 @@
 // Shared device helpers for the e4b kernels (sm_100a).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -47,6 +48,24 @@ inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, dim3 block, size_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets a kernel use up to `most` bytes of dynamic shared memory on the current
+// device, once for each device (the attribute belongs to it). `known`: the
+// kernel's own table; always the same `most` for a kernel, so that threads that
+// come here together set the same.
+struct SmemAllowed {
+  std::atomic<bool> on[64] = {};
+};
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int most, SmemAllowed& known) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && known.on[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (err == cudaSuccess && kept) known.on[dev].store(true, std::memory_order_release);
+  return err;
 }
 
 // ------------------------------------------------------------------ bf16

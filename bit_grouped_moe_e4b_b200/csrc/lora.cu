@@ -599,9 +599,10 @@ cudaError_t launch_expand_of(const Adapters& d, Expand e, cudaStream_t st, int s
   int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, kTile);
   if (grid > int64_t(sms) * kExpandCtas<KS, GLU>) grid = int64_t(sms) * kExpandCtas<KS, GLU>;
   auto kernel = expand_kernel<KS, GLU, ACT, WT>;
-  const int smem = 2 * kSixteens * KS * 64 * 16 + (e.base ? (kAhead + 1) * 2 * strips * kThreads * 16 : 0);
-  // set on every call: the attribute belongs to the device that is current
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int staged = 2 * kSixteens * KS * 64 * 16, ring = (kAhead + 1) * 2 * strips * kThreads * 16;
+  const int smem = staged + (e.base ? ring : 0);
+  static SmemAllowed allowed;
+  const cudaError_t err = allow_smem(kernel, staged + ring, allowed);
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, dim3(unsigned(grid)), dim3(kThreads), smem, st, d, e);
 }

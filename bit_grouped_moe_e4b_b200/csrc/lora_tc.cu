@@ -820,8 +820,8 @@ template <bool OUT, bool GRAD, int RP>
 cudaError_t launch(const CUtensorMap& tile, const CUtensorMap& edge, const CUtensorMap& w, const Pass& p, cudaStream_t st, int sms) {
   auto kernel = contract_kernel<OUT, GRAD, RP>;
   const uint32_t smem = layout_of(p, OUT, GRAD, RP).total;
-  // set on every call: the attribute belongs to the device that is current
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static SmemAllowed allowed;
+  const cudaError_t err = allow_smem(kernel, int(kSmemLimit), allowed);
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, dim3(sms), dim3(kThreads), smem, st, tile, edge, w, p);
 }

@@ -449,9 +449,23 @@ def _vec(name, t, dtype, shape, dev):
     return t.data_ptr()
 
 
+def _vec1(name, t, dtype, n, dev):
+    """_vec of n values."""
+    if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+        _refuse(name, t, dtype, (n,), dev, False)
+    return t.data_ptr()
+
+
 def _rows(name, t, n, width, dev):
     """(address, row stride) of bf16 rows [n, width] on device dev."""
-    if t.dtype is not _BF16 or t.shape != (n, width) or t.get_device() != dev or dev < 0:
+    if t.shape != (n, width):
+        _refuse(name, t, _BF16, (n, width), dev, True)
+    return _same_rows(name, t, n, width, dev)
+
+
+def _same_rows(name, t, n, width, dev):
+    """_rows of a tensor whose shape is known to be [n, width]."""
+    if t.dtype is not _BF16 or t.get_device() != dev or dev < 0:
         _refuse(name, t, _BF16, (n, width), dev, True)
     if n < 2:  # a single row, or none, may carry any stride
         ld = -(-width // 8) * 8
@@ -470,6 +484,8 @@ def _matrix(name, t):
     return t.shape
 
 
+# the device of a process that has a CUDA tensor in hand
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
@@ -482,7 +498,7 @@ def _call(name, dev, stream, *args):
         s = _raw_stream(dev)
     else:
         s = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = f(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -498,8 +514,9 @@ def e4b_permute(x, perm, offsets, xs, *, top_k, stream=None):
     if R > T * top_k:
         raise ValueError("xs has more rows than there are slots")
     E = offsets.numel() - 1
-    _call("e4b_permute", dev, stream, *_rows("x", x, T, H, dev), T, H, _vec("perm", perm, _I32, (T * top_k,), dev),
-          top_k, _vec("offsets", offsets, _I64, (E + 1,), dev), E, R, *_rows("xs", xs, R, H, dev))
+    _call("e4b_permute", dev, stream, *_same_rows("x", x, T, H, dev), T, H,
+          _vec1("perm", perm, _I32, T * top_k, dev), top_k, _vec1("offsets", offsets, _I64, E + 1, dev), E, R,
+          *_rows("xs", xs, R, H, dev))
 
 
 def e4b_permute_backward(dxs, inv_perm, dx, *, top_k, stream=None):
@@ -507,7 +524,7 @@ def e4b_permute_backward(dxs, inv_perm, dx, *, top_k, stream=None):
     T, H = _matrix("dx", dx)
     R, dev = _matrix("dxs", dxs)[0], dx.get_device()
     _call("e4b_permute_backward", dev, stream, *_rows("dxs", dxs, R, H, dev), R, H,
-          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev), T, top_k, *_rows("dx", dx, T, H, dev))
+          _vec1("inv_perm", inv_perm, _I32, T * top_k, dev), T, top_k, *_same_rows("dx", dx, T, H, dev))
 
 
 def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
@@ -516,9 +533,9 @@ def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
     T, H = _matrix("y", y)
     R, dev = _matrix("ys", ys)[0], y.get_device()
     _call("e4b_unpermute", dev, stream, *_rows("ys", ys, R, H, dev), R, H,
-          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev),
+          _vec1("inv_perm", inv_perm, _I32, T * top_k, dev),
           None if gates is None else _vec("gates", gates, _F32, (T, top_k), dev), T, top_k,
-          *_rows("y", y, T, H, dev))
+          *_same_rows("y", y, T, H, dev))
 
 
 def e4b_unpermute_backward(dy, ys, inv_perm, gates, dys, dgates, *, top_k, stream=None):
@@ -529,9 +546,9 @@ def e4b_unpermute_backward(dy, ys, inv_perm, gates, dys, dgates, *, top_k, strea
     if (ys is None and dys is None) or (ys is None and dgates is not None) or (dys is None and dgates is None):
         raise ValueError("ys is needed for dgates, dys or dgates for a result")
     R = _matrix("ys", dys if ys is None else ys)[0]
-    _call("e4b_unpermute_backward", dev, stream, *_rows("dy", dy, T, H, dev),
+    _call("e4b_unpermute_backward", dev, stream, *_same_rows("dy", dy, T, H, dev),
           *((None, 0) if ys is None else _rows("ys", ys, R, H, dev)), R, H,
-          _vec("inv_perm", inv_perm, _I32, (T * top_k,), dev),
+          _vec1("inv_perm", inv_perm, _I32, T * top_k, dev),
           None if gates is None else _vec("gates", gates, _F32, (T, top_k), dev), T, top_k,
           *((None, 0) if dys is None else _rows("dys", dys, R, H, dev)),
           None if dgates is None else _vec("dgates", dgates, _F32, (T, top_k), dev))
@@ -545,8 +562,8 @@ def _glu_args(gu, offsets, layout, act, alpha, limit):
     a = GluArgs(0, LAYOUT[layout], ACT[act], alpha, limit, I2 // 2, R)
     if offsets is not None:
         a.E = offsets.numel() - 1
-        a.offsets = _vec("offsets", offsets, _I64, (a.E + 1,), dev)
-    a.gu, a.ld_gu = _rows("gu", gu, R, I2, dev)
+        a.offsets = _vec1("offsets", offsets, _I64, a.E + 1, dev)
+    a.gu, a.ld_gu = _same_rows("gu", gu, R, I2, dev)
     return a, R, I2 // 2, dev
 
 
@@ -585,9 +602,9 @@ def _lora_args(a, b, offsets, scale, row, n, dev):
     N = b.shape[1]
     R_max = n if row is None else row.numel()
     return LoraArgs(G, r, N, K, R_max, _vec("a", a, _BF16, (G, r, K), dev), _vec("b", b, _BF16, (G, N, r), dev),
-                    None if scale is None else _vec("scale", scale, _F32, (G,), dev),
-                    _vec("offsets", offsets, _I64, (G + 1,), dev),
-                    None if row is None else _vec("row", row, _I32, (R_max,), dev), n)
+                    None if scale is None else _vec1("scale", scale, _F32, G, dev),
+                    _vec1("offsets", offsets, _I64, G + 1, dev),
+                    None if row is None else _vec1("row", row, _I32, R_max, dev), n)
 
 
 def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=None, row=None, layout="halves",
@@ -597,9 +614,9 @@ def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=N
     those that are given are written. a [G, r, K], b [G, N, r], x [*, K], base
     and y [*, N], h [*, N/2], s fp32 [R_max, r], scale fp32 [G], row [R_max],
     status int32 [1], zeroed by the caller."""
-    n, dev = _matrix("x", x)[0], x.get_device()
+    (n, K), dev = _matrix("x", x), x.get_device()
     p = _lora_args(a, b, offsets, scale, row, n, dev)
-    p.x, p.ld_x = _rows("x", x, n, p.K, dev)
+    p.x, p.ld_x = (_same_rows if K == p.K else _rows)("x", x, n, p.K, dev)
     if s is not None:
         p.s = _vec("s", s, _F32, (p.R_max, p.r), dev)
     if base is not None:
@@ -610,9 +627,9 @@ def e4b_lora(a, b, x, offsets, ws, *, base=None, y=None, h=None, s=None, scale=N
         p.h, p.ld_h = _rows("h", h, n, p.N // 2, dev)
         p.gate_up_layout, p.activation, p.glu_alpha, p.glu_limit = LAYOUT[layout], ACT[act], alpha, limit
     if status is not None:
-        p.status = _vec("status", status, _I32, (1,), dev)
+        p.status = _vec1("status", status, _I32, 1, dev)
     nb = ws.numel()
-    _call("e4b_lora", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb, flags)
+    _call("e4b_lora", dev, stream, p, _vec1("ws", ws, _U8, nb, dev), nb, flags)
 
 
 def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=None, db=None, accumulate=False,
@@ -622,9 +639,9 @@ def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=
     scale[g] B_g^T dy[i]; those of dx, da (fp32 [G, r, K]) and db (fp32 [G, N, r])
     that are given. accumulate: da and db are added to. x may be None without
     da, s without db."""
-    n, dev = _matrix("dy", dy)[0], dy.get_device()
+    (n, N), dev = _matrix("dy", dy), dy.get_device()
     p = _lora_args(a, b, offsets, scale, row, n, dev)
-    p.dy, p.ld_dy = _rows("dy", dy, n, p.N, dev)
+    p.dy, p.ld_dy = (_same_rows if N == p.N else _rows)("dy", dy, n, p.N, dev)
     if x is not None:
         p.x, p.ld_x = _rows("x", x, n, p.K, dev)
     if s is not None:
@@ -638,9 +655,9 @@ def e4b_lora_backward(a, b, x, s, dy, offsets, ws, *, dx=None, dx_base=None, da=
     if db is not None:
         p.db = _vec("db", db, _F32, (p.G, p.N, p.r), dev)
     if status is not None:
-        p.status = _vec("status", status, _I32, (1,), dev)
+        p.status = _vec1("status", status, _I32, 1, dev)
     nb = ws.numel()
-    _call("e4b_lora_backward", dev, stream, p, _vec("ws", ws, _U8, (nb,), dev), nb,
+    _call("e4b_lora_backward", dev, stream, p, _vec1("ws", ws, _U8, nb, dev), nb,
           flags | (FLAG_ACCUMULATE if accumulate else 0))
 
 
