@@ -15,10 +15,11 @@
 // makes the fp32 gradients as exact as fp32 products: two terms left a relative
 // error of 2^-17 a product. The terms lie side by side as columns of one B
 // operand (N = 3 * rank) up to rank 32, and are added when TMEM is read: three
-// MMAs into one accumulator would read the tile from shared memory three times.
+// MMAs into one accumulator would read the tile from shared memory, and issue,
+// three times.
 // An MMA truncates its sum, so that n of them in one accumulator leave it 1.2e-8
 // n too small (2.1e-6 after 128, measured), and dA inherits t's share. Sums
-// therefore leave TMEM after kOutChain column tiles and grad_chain row tiles and
+// therefore leave TMEM after kOutChain column tiles and kGradChain row tiles and
 // go on in fp32 additions: within 1e-6, as products and sums of fp32 are.
 //
 // One persistent CTA per SM. The work is the list of (column block, row tile)
@@ -30,7 +31,9 @@
 // the sizes alone.
 //   warp 0       TMA: W's box, and the tile's where its rows lie together (in
 //                boxes of 32 rows at a group's end)
-//   warp 1       TMEM and the single-thread MMA issue
+//   warp 1       TMEM, the MMAs of out; warp 14 those of grad (an MMA this narrow
+//                takes less time than its issue, about 60 cycles: one thread for
+//                both took 1.0 us a tile, above the 0.74 us that HBM needs)
 //   warps 2-5    v's terms of each row tile, in the operand's layout
 //   warps 6-9    TMEM to out and grad
 //   warps 10-13  mapped rows, by cp.async into the same swizzled boxes (four-row
@@ -52,16 +55,16 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 448;
-constexpr int kLoadWarp = 10, kLoadWarps = 4;
+constexpr int kThreads = 480;
+constexpr int kLoadWarp = 10, kLoadWarps = 4, kGradWarp = 14;
 static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
 constexpr uint32_t kZBytes = 2 * kBox;           // a tile
-constexpr int kOutChain = 2;                     // tiles of eight MMAs
-// Tiles of eight MMAs, or of 24 (three terms into one accumulator, of which the
-// small ones hardly move the sum).
-__host__ __device__ constexpr int grad_chain(int rp) { return rp <= 32 ? 8 : 2; }
+constexpr int kOutChain = 2, kGradChain = 8;     // tiles of eight MMAs
+// TMEM columns of a tile's gradient: the three terms' sums, or above rank 32,
+// where these would leave room for two tiles, hi's and the others'.
+__host__ __device__ constexpr int grad_width(int rp) { return rp <= 32 ? 3 * rp : 2 * rp; }
 constexpr int kMaxStages = 6;
 constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
 constexpr uint32_t kSmemLimit = 232448;
@@ -179,7 +182,8 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   uint64_t* v_full = t_empty + 2;
   uint64_t* v_empty = v_full + 2;
   uint64_t* g_full = v_empty + 2;
-  uint64_t* g_empty = g_full + 1;  // [kMaxChunks]
+  uint64_t* drained = g_full + 1;      // [2]
+  uint64_t* g_empty = drained + 2;     // [kMaxChunks]
   int64_t* s_sum = reinterpret_cast<int64_t*>(g_empty + kMaxChunks);  // [kThreads / 32]
   int64_t* s_start = s_sum + kThreads / 32;                           // group, tile
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_start + 2);
@@ -197,11 +201,12 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&loaded[s], kLoadWarps);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], OUT && GRAD ? 2 : 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&t_full[b], 1);
       mbar_init(&t_empty[b], 128);
+      mbar_init(&drained[b], 1);
       mbar_init(&v_full[b], 128);
       mbar_init(&v_empty[b], 1);
     }
@@ -222,8 +227,8 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
 
   const int all_chunks = int((p.C + kTile - 1) / kTile);
   constexpr int rp = RP;
-  constexpr bool merged = RP <= 32;
-  constexpr int gw = merged ? 3 * rp : rp;  // TMEM columns of a tile's gradient
+  constexpr bool side_by_side = RP <= 32;  // all three terms, or hi and mid + lo
+  constexpr int gw = grad_width(RP);       // TMEM columns of a tile's gradient
   const uint32_t d_grad = tmem + (OUT ? 2 * rp : 0);
   Walk wk(p.offsets, p.G, p.R_max, run, s_start);
   auto chunks_of = [&](int cb) { return min(p.chunks, all_chunks - cb * p.chunks); };
@@ -239,6 +244,13 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   const bool loaders = GRAD || p.row;
   // rows of the tile that the MMAs read, or whose results count
   auto rows_read = [&]() { return GRAD ? (wk.n() + 15) / 16 * 16 : wk.n(); };
+
+  // the MMAs that this thread issued have to finish before TMEM is freed
+  auto drain = [&](uint64_t* bar) {
+    if (!*s_abort) return;  // the results' warps have waited for them
+    mma_commit(bar);
+    mbar_wait_bounded(bar, 0, kWaitPolls, nullptr);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
@@ -286,26 +298,59 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         mbar_wait_bounded(&full[q % p.stages], uint32_t(q / p.stages) & 1u, kWaitPolls, nullptr);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint32_t id_out = idesc_bf16_f32(kTile, rp) | (p.w_t ? 1u << 16 : 0u);
-      const uint32_t id_grad = idesc_bf16_f32(kTile, gw) | (1u << 15) | (1u << 16);  // both MN-major
-      const uint32_t vk = uint32_t(3 * rp / 8) * 128;  // bytes of 8 positions of v's terms
+    // ------------------------------------------------- MMAs along the columns
+    if (OUT && lane == 0) {
+      const uint32_t id = idesc_bf16_f32(kTile, rp) | (p.w_t ? 1u << 16 : 0u);
       // W's steps along its 128 columns: 16 of them, 64 of them
       const uint32_t w_step = p.w_t ? 32 * rp : 32, w_half = 128 * rp;
       const uint32_t z0 = smem_u32(smem);
-      const uint64_t zk = sw128_kmajor_desc(z0), zm = sw128_mnmajor_desc(z0, kBox, 1024);
+      const uint64_t zd0 = sw128_kmajor_desc(z0);
       const uint64_t wd0 = p.w_t ? span_desc(z0 + kZBytes, 2 * rp) : sw128_kmajor_desc(z0 + kZBytes);
-      const uint64_t vd0 = plain_desc(z0 + lay.terms, vk, 128);
-      Ring st(p.stages), vr(p.vbufs), tr(2);
+      Ring st(p.stages), tr(2);
+      bool aborted = false;
+      for (int64_t k = 0; k < count && !aborted; ++k) {
+        const int nc = chunks_of(wk.cb);
+        for (int c = 0; c < nc; ++c, st.next()) {
+          const int link = c % kOutChain;
+          if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
+              (loaders && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
+              (link == 0 && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort))) {
+            give_up();
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = st.slot * lay.stage, d = tmem + tr.slot * rp;
+          const uint64_t zd = step_desc(zd0, at), wd = step_desc(wd0, at);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ss(d, step_desc(zd, (kk >> 2) * kBox + (kk & 3) * 32),
+                        step_desc(wd, uint32_t(kk >> 2) * w_half + uint32_t(kk & 3) * w_step), id, (link | kk) ? 1u : 0u);
+          mma_commit(&empty[st.slot]);
+          if (link == kOutChain - 1 || c + 1 == nc) {
+            mma_commit(&t_full[tr.slot]);
+            tr.next();
+          }
+        }
+        if (k + 1 < count) wk.next();
+      }
+      drain(&drained[0]);
+    }
+  } else if (warp == kGradWarp) {
+    // ----------------------------------------------- MMAs along the positions
+    if (GRAD && lane == 0) {
+      constexpr uint32_t mn_major = (1u << 15) | (1u << 16);  // both operands
+      const uint32_t id = idesc_bf16_f32(kTile, gw) | mn_major, id_lo = idesc_bf16_f32(kTile, rp) | mn_major;
+      constexpr uint32_t vk = uint32_t(3 * rp / 8) * 128;  // bytes of 8 positions of v's terms
+      const uint32_t z0 = smem_u32(smem);
+      const uint64_t zd0 = sw128_mnmajor_desc(z0, kBox, 1024), vd0 = plain_desc(z0 + lay.terms, vk, 128);
+      Ring st(p.stages), vr(p.vbufs);
       uint32_t g_phase = 0;
-      uint64_t* last_bar = nullptr;
-      uint32_t last_ph = 0;
       bool aborted = false;
       bool fresh = true;  // first row tile of a chain
       int chain = 0;
       for (int64_t k = 0; k < count && !aborted; ++k) {
-        if (GRAD && !mbar_wait_bounded(&v_full[vr.slot], vr.parity, p.limit, s_abort)) {
+        if (!mbar_wait_bounded(&v_full[vr.slot], vr.parity, p.limit, s_abort)) {
           give_up();
           break;
         }
@@ -315,66 +360,33 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         uint32_t d = d_grad;
         for (int c = 0; c < nc; ++c, d += gw, st.next()) {
           if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
-              (loaders && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
-              (OUT && c % kOutChain == 0 && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort)) ||
-              (GRAD && fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
+              !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort) ||
+              (fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
             give_up();
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t at = st.slot * lay.stage;
-          if (OUT) {
-            const uint64_t zd = step_desc(zk, at), wd = step_desc(wd0, at);
+          if (fresh) g_phase ^= 1u << c;
+          const uint64_t zd = step_desc(zd0, st.slot * lay.stage);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(tmem + tr.slot * rp, step_desc(zd, (kk >> 2) * kBox + (kk & 3) * 32),
-                          step_desc(wd, uint32_t(kk >> 2) * w_half + uint32_t(kk & 3) * w_step), id_out,
-                          (c % kOutChain | kk) ? 1u : 0u);
-          }
-          if (GRAD) {
-            if (fresh) g_phase ^= 1u << c;
-            const uint64_t zd = step_desc(zm, at);
-            if constexpr (merged) {
-              uint64_t vs = vd;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                if (kk < steps) mma_bf16_ss(d, step_desc(zd, kk * 2048), vs, id_grad, !fresh || kk ? 1u : 0u);
-                vs = step_desc(vs, 2 * vk);
-              }
-            } else {  // the small terms first
-              uint64_t vs = vd;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                if (kk < steps) {
-                  mma_bf16_ss(d, step_desc(zd, kk * 2048), step_desc(vs, 32 * rp), id_grad, !fresh || kk ? 1u : 0u);
-                  mma_bf16_ss(d, step_desc(zd, kk * 2048), step_desc(vs, 16 * rp), id_grad, 1u);
-                  mma_bf16_ss(d, step_desc(zd, kk * 2048), vs, id_grad, 1u);
-                }
-                vs = step_desc(vs, 2 * vk);
-              }
-            }
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk >= steps) break;
+            const uint64_t zs = step_desc(zd, kk * 2048), vs = step_desc(vd, kk * 2 * vk);
+            mma_bf16_ss(d, zs, vs, id, !fresh || kk ? 1u : 0u);
+            if constexpr (!side_by_side) mma_bf16_ss(d + rp, zs, step_desc(vs, 32 * rp), id_lo, 1u);
           }
           mma_commit(&empty[st.slot]);
-          last_bar = &empty[st.slot];
-          last_ph = st.parity;
-          if (OUT && (c % kOutChain == kOutChain - 1 || c + 1 == nc)) {
-            mma_commit(&t_full[tr.slot]);
-            tr.next();
-          }
         }
         if (aborted) break;
-        if (GRAD) {
-          mma_commit(&v_empty[vr.slot]);
-          fresh = ++chain == grad_chain(RP) || wk.last();
-          if (fresh || k + 1 == count) mma_commit(g_full);
-          if (fresh) chain = 0;
-        }
+        mma_commit(&v_empty[vr.slot]);
+        fresh = ++chain == kGradChain || wk.last();
+        if (fresh || k + 1 == count) mma_commit(g_full);
+        if (fresh) chain = 0;
         vr.next();
         if (k + 1 < count) wk.next();
       }
-      // the MMAs issued so far have to finish before TMEM is freed
-      if (*s_abort && last_bar) mbar_wait_bounded(last_bar, last_ph, kWaitPolls, nullptr);
+      drain(&drained[1]);
     }
   } else if (warp < 6) {
     // ------------------------------------------- v's terms, a thread a position
@@ -416,7 +428,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         if (k + 1 < count) wk.next();
       }
     }
-  } else if (warp >= kLoadWarp) {
+  } else if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
     // ---------------------------- rows that TMA does not bring, or not alone
     const int w4 = warp - kLoadWarp;
     if (p.row) {
@@ -550,7 +562,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           part = 2 * int(blockIdx.x) + (k ? 1 : 0);
           if (!direct && m == 0) p.notes[part] = Note{wk.g, wk.cb, wk.first()};
         }
-        const bool fresh = ++chain == grad_chain(RP) || wk.last();
+        const bool fresh = ++chain == kGradChain || wk.last();
         if (fresh || k + 1 == count) {
           chain = 0;
           if (!warp_wait(g_full, chains++ & 1u, p.limit, s_abort)) {
@@ -594,9 +606,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
               uint32_t v[16];
               const uint32_t from = d_grad + lanes + uint32_t(c * gw + j0);
               tmem_ld_32x32b_x16(from, v);
-              if constexpr (merged) {
-                uint32_t v1[16], v2[16];
-                tmem_ld_32x32b_x16(from + rp, v1);
+              uint32_t v1[16];
+              tmem_ld_32x32b_x16(from + rp, v1);
+              if constexpr (side_by_side) {
+                uint32_t v2[16];
                 tmem_ld_32x32b_x16(from + 2 * rp, v2);
                 tmem_ld_wait();
 #pragma unroll
@@ -605,7 +618,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
               } else {
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v1[j]) + __uint_as_float(v[j]);
               }
               if (j0 + 16 >= RP) {
                 tc_fence_before();
@@ -755,7 +768,7 @@ struct Plan {
 Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
   Plan q;
   q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
-  const int gw = q.rp <= 32 ? 3 * q.rp : q.rp;
+  const int gw = grad_width(q.rp);
   int most = grad ? (512 - (out ? 2 * q.rp : 0)) / gw : 64;
   if (grad && most > kMaxChunks) most = kMaxChunks;
   const int64_t all = (C + kTile - 1) / kTile;
@@ -766,7 +779,7 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   q.chunks = 0;
   for (int64_t c = 1; c <= most && c <= all; ++c) {
     const int64_t blocks = (all + c - 1) / c, items = blocks * tiles;
-    double t = double((items + sms - 1) / sms) * (double(c) + (grad && q.rp == 64 ? 2.5 : 0.5));
+    double t = double((items + sms - 1) / sms) * (double(c) + (grad && q.rp == 64 ? 1.5 : 0.5));
     if (grad) t += 0.5 * double(c);
     if (out && blocks > 1) t += double(items) * r / (32.0 * sms);
     if (!q.chunks || t <= best) {
