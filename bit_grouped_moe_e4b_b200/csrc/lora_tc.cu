@@ -147,24 +147,31 @@ E4B_DEV bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit, const vol
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-E4B_DEV float finite_rest(float v, float h) { return fabsf(h) < INFINITY ? v - h : 0.f; }
+// (a, b) -= the bf16 pair h.
+E4B_DEV void less(float& a, float& b, uint32_t h) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"((h << 16) ^ 0x80000000u), "r"((h & 0xFFFF0000u) ^ 0x80000000u));
+}
 
 // Eight values as three bf16 terms; infinities and NaN have only the first.
-E4B_DEV void split3(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
-  uint32_t t[3][4];
+E4B_DEV void split3(float4 x, float4 y, float w, uint4 (&t)[3]) {
+  float v[8] = {w * x.x, w * x.y, w * x.z, w * x.w, w * y.x, w * y.y, w * y.z, w * y.w};
+  uint32_t q[3][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a = v[2 * i], b = v[2 * i + 1];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      t[k][i] = pack_bf16x2(a, b);
-      a = finite_rest(a, __uint_as_float(t[k][i] << 16));
-      b = finite_rest(b, __uint_as_float(t[k][i] & 0xFFFF0000u));
-    }
+    float &a = v[2 * i], &b = v[2 * i + 1];
+    const uint32_t h = q[0][i] = pack_bf16x2(a, b);
+    less(a, b, h);
+    if ((h & 0x7F80u) == 0x7F80u) a = 0.f;
+    if ((h & 0x7F800000u) == 0x7F800000u) b = 0.f;
+    q[1][i] = pack_bf16x2(a, b);
+    less(a, b, q[1][i]);
+    q[2][i] = pack_bf16x2(a, b);
   }
-  hi = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
-  mid = make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
-  lo = make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) t[k] = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
 }
 
 template <bool OUT, bool GRAD, int RP>  // RP: the rank's operand width, 16, 32 or 64
@@ -389,38 +396,46 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       drain(&drained[1]);
     }
   } else if (warp < 6) {
-    // ------------------------------------------- v's terms, a thread a position
+    // ------------------------------------------------------------ v's terms
+    // A thread takes eights of a position's values, as many as the operand has
+    // eights (GR). Neighbouring lanes take eight positions, whose 16-byte stores
+    // fill a line of banks, by up to four eights, so that a load touches whole
+    // sectors of few lines. The terms are made before the wait for their buffer.
     if constexpr (GRAD) {
-      const int m = tid - 64;
-      uint8_t* mine_at = smem + lay.terms + (m >> 3) * (3 * rp / 8) * 128 + (m & 7) * 16;
+      constexpr int GR = RP / 8, LG = GR < 4 ? GR : 4;  // eights of a position; of them side by side in a warp
+      constexpr int LP = 32 / LG;                       // positions side by side
+      const int eight0 = (lane >> 3) % LG, m0 = (warp - 2) * 32 + (lane >> 3) / LG * 8 + (lane & 7);
       Ring vr(p.vbufs);
       for (int64_t k = 0; k < count; ++k) {
-        const int64_t pos = wk.row0() + m;
-        bool in = m < wk.n();
-        if (in && p.row) {
-          const int32_t at = __ldg(p.row + pos);
-          in = at >= 0 && at < p.rows;
-        }
+        const int64_t row0 = wk.row0();
+        const int n = wk.n();
         const float w = p.scale_v && p.scale ? __ldg(p.scale + wk.g) : 1.f;
-        float4 x[RP / 4];
+        float4 x[GR][2];
 #pragma unroll
-        for (int j = 0; j < RP / 4; ++j)
-          x[j] = in && 4 * j < p.r ? __ldg(reinterpret_cast<const float4*>(p.v + pos * p.r) + j)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int u = 0; u < GR; ++u) {
+          const int m = m0 + u % LG * LP, j = 8 * (eight0 + u / LG * LG);
+          bool in = m < n && j < p.r;
+          if (in && p.row) {
+            const int32_t at = __ldg(p.row + row0 + m);
+            in = at >= 0 && at < p.rows;
+          }
+          const float4* from = reinterpret_cast<const float4*>(p.v + (row0 + m) * p.r + j);
+          x[u][0] = in ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[u][1] = in ? __ldg(from + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        uint4 t[GR][3];
+#pragma unroll
+        for (int u = 0; u < GR; ++u) split3(x[u][0], x[u][1], w, t[u]);
         if (!warp_wait(&v_empty[vr.slot], vr.parity ^ 1u, p.limit, s_abort)) {
           give_up();
           break;
         }
 #pragma unroll
-        for (int j = 0; j < RP / 8; ++j) {
-          const float f[8] = {w * x[2 * j].x, w * x[2 * j].y, w * x[2 * j].z, w * x[2 * j].w,
-                              w * x[2 * j + 1].x, w * x[2 * j + 1].y, w * x[2 * j + 1].z, w * x[2 * j + 1].w};
-          uint4 hi, mid, lo;
-          split3(f, hi, mid, lo);
-          uint8_t* dst = mine_at + vr.slot * 6 * kTile * rp + j * 128;
-          *reinterpret_cast<uint4*>(dst) = hi;
-          *reinterpret_cast<uint4*>(dst + rp * 16) = mid;
-          *reinterpret_cast<uint4*>(dst + rp * 32) = lo;
+        for (int u = 0; u < GR; ++u) {
+          const int m = m0 + u % LG * LP, eight = eight0 + u / LG * LG;
+          uint8_t* dst = smem + lay.terms + vr.slot * 6 * kTile * rp + ((m >> 3) * (3 * GR) + eight) * 128 + (m & 7) * 16;
+#pragma unroll
+          for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * GR * 128) = t[u][q];
         }
         fence_proxy_async_smem();
         mbar_arrive(&v_full[vr.slot]);
