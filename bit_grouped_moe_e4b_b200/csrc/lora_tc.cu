@@ -37,12 +37,15 @@
 //   warps 2-5    v's terms of each row tile, in the operand's layout
 //   warps 6-9    TMEM to out and grad
 //   warps 10-13  mapped rows, by cp.async into the same swizzled boxes (four-row
-//                TMA gathers took 45 ns each: three times as long as whole boxes),
-//                and zeros in place of the rows behind a group's end that a
-//                gradient's MMAs read, so that no other group's values meet these
+//                TMA gathers took 45 ns each: three times as long as whole boxes);
+//                without a map they share the terms
+//   warp 15      zeros in place of the rows behind a group's end that a gradient's
+//                MMAs read, so that no other group's values meet these
 // Every wait is bounded; one that gives up records E4B_ERR_DEVICE_TIMEOUT,
 // stops all roles, drains the copies and MMAs in flight, frees TMEM and returns.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "lora_tc.h"
@@ -55,8 +58,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 480;
-constexpr int kLoadWarp = 10, kLoadWarps = 4, kGradWarp = 14;
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 10, kLoadWarps = 4, kGradWarp = 14, kZeroWarp = 15;
 static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
@@ -207,14 +210,14 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&loaded[s], kLoadWarps);
+      mbar_init(&loaded[s], p.row ? kLoadWarps : 1);
       mbar_init(&empty[s], OUT && GRAD ? 2 : 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&t_full[b], 1);
       mbar_init(&t_empty[b], 128);
       mbar_init(&drained[b], 1);
-      mbar_init(&v_full[b], 128);
+      mbar_init(&v_full[b], p.row ? 128 : 256);
       mbar_init(&v_empty[b], 1);
     }
     mbar_init(g_full, 1);
@@ -244,13 +247,67 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     record_status(p.status, E4B_ERR_DEVICE_TIMEOUT);
   };
 
-  // The loaders have a part in every stage or in none: a parity wait must never
-  // be two uses of its barrier away, so no role may skip stages that another
-  // walks. Without grad the rows past a group's end only make results that are
-  // not written.
-  const bool loaders = GRAD || p.row;
+  // Between a stage's copies and its MMAs along the positions there is always a
+  // warp that completes it (`loaded`): a parity wait must never be two uses of
+  // its barrier away, so no role may skip stages that another walks. The MMAs
+  // along the columns take the stage as TMA completes it, with rows past a
+  // group's end that only make results that are not written.
   // rows of the tile that the MMAs read, or whose results count
   auto rows_read = [&]() { return GRAD ? (wk.n() + 15) / 16 * 16 : wk.n(); };
+
+  // v's terms, by four warps or (without a map) eight. A thread takes eights of a
+  // position's values, GR of which the operand has. Neighbouring lanes take eight
+  // positions, whose 16-byte stores fill a line of banks, by up to four eights, so
+  // that a load touches whole sectors of few lines. The terms are made before the
+  // wait for their buffer.
+  auto terms_by = [&](auto warps, int first) {
+    constexpr int GR = RP / 8, LG = GR < 4 ? GR : 4;  // eights of a position; of them side by side in a warp
+    constexpr int LP = 32 / LG, PS = kTile / warps.value / LP, UNITS = PS * (GR / LG);  // positions side by side, after one another
+    const int eight0 = (lane >> 3) % LG, m0 = first * (kTile / warps.value) + (lane >> 3) / LG * 8 + (lane & 7);
+    Ring vr(p.vbufs);
+    for (int64_t k = 0; k < count; ++k) {
+      const int64_t row0 = wk.row0();
+      const int n = wk.n();
+      const float w = p.scale_v && p.scale ? __ldg(p.scale + wk.g) : 1.f;
+      float4 x[UNITS][2];
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int m = m0 + u % PS * LP, j = 8 * (eight0 + u / PS * LG);
+        bool in = m < n && j < p.r;
+        if (in && p.row) {
+          const int32_t at = __ldg(p.row + row0 + m);
+          in = at >= 0 && at < p.rows;
+        }
+        const float4* from = reinterpret_cast<const float4*>(p.v + (row0 + m) * p.r + j);
+        x[u][0] = in ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u][1] = in ? __ldg(from + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      uint4 t[UNITS][3];
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) split3(x[u][0], x[u][1], w, t[u]);
+      if (!warp_wait(&v_empty[vr.slot], vr.parity ^ 1u, p.limit, s_abort)) {
+        give_up();
+        break;
+      }
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int m = m0 + u % PS * LP, eight = eight0 + u / PS * LG;
+        uint8_t* dst = smem + lay.terms + vr.slot * 6 * kTile * rp + ((m >> 3) * (3 * GR) + eight) * 128 + (m & 7) * 16;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * GR * 128) = t[u][q];
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&v_full[vr.slot]);
+      vr.next();
+      if (k + 1 < count) wk.next();
+    }
+  };
+  auto make_terms = [&](int first) {
+    if constexpr (GRAD) {
+      if (p.row) terms_by(std::integral_constant<int, 4>{}, first);
+      else terms_by(std::integral_constant<int, 8>{}, first);
+    }
+  };
 
   // the MMAs that this thread issued have to finish before TMEM is freed
   auto drain = [&](uint64_t* bar) {
@@ -320,7 +377,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         for (int c = 0; c < nc; ++c, st.next()) {
           const int link = c % kOutChain;
           if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
-              (loaders && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
+              (p.row && !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort)) ||
               (link == 0 && !mbar_wait_bounded(&t_empty[tr.slot], tr.parity ^ 1u, p.limit, s_abort))) {
             give_up();
             aborted = true;
@@ -366,8 +423,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
         const uint64_t vd = step_desc(vd0, vr.slot * 6 * kTile * rp);
         uint32_t d = d_grad;
         for (int c = 0; c < nc; ++c, d += gw, st.next()) {
-          if (!mbar_wait_bounded(&full[st.slot], st.parity, p.limit, s_abort) ||
-              !mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort) ||
+          if (!mbar_wait_bounded(&loaded[st.slot], st.parity, p.limit, s_abort) ||
               (fresh && !mbar_wait_bounded(&g_empty[c], ((g_phase >> c) & 1u) ^ 1u, p.limit, s_abort))) {
             give_up();
             aborted = true;
@@ -396,57 +452,13 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       drain(&drained[1]);
     }
   } else if (warp < 6) {
-    // ------------------------------------------------------------ v's terms
-    // A thread takes eights of a position's values, as many as the operand has
-    // eights (GR). Neighbouring lanes take eight positions, whose 16-byte stores
-    // fill a line of banks, by up to four eights, so that a load touches whole
-    // sectors of few lines. The terms are made before the wait for their buffer.
-    if constexpr (GRAD) {
-      constexpr int GR = RP / 8, LG = GR < 4 ? GR : 4;  // eights of a position; of them side by side in a warp
-      constexpr int LP = 32 / LG;                       // positions side by side
-      const int eight0 = (lane >> 3) % LG, m0 = (warp - 2) * 32 + (lane >> 3) / LG * 8 + (lane & 7);
-      Ring vr(p.vbufs);
-      for (int64_t k = 0; k < count; ++k) {
-        const int64_t row0 = wk.row0();
-        const int n = wk.n();
-        const float w = p.scale_v && p.scale ? __ldg(p.scale + wk.g) : 1.f;
-        float4 x[GR][2];
-#pragma unroll
-        for (int u = 0; u < GR; ++u) {
-          const int m = m0 + u % LG * LP, j = 8 * (eight0 + u / LG * LG);
-          bool in = m < n && j < p.r;
-          if (in && p.row) {
-            const int32_t at = __ldg(p.row + row0 + m);
-            in = at >= 0 && at < p.rows;
-          }
-          const float4* from = reinterpret_cast<const float4*>(p.v + (row0 + m) * p.r + j);
-          x[u][0] = in ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
-          x[u][1] = in ? __ldg(from + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        uint4 t[GR][3];
-#pragma unroll
-        for (int u = 0; u < GR; ++u) split3(x[u][0], x[u][1], w, t[u]);
-        if (!warp_wait(&v_empty[vr.slot], vr.parity ^ 1u, p.limit, s_abort)) {
-          give_up();
-          break;
-        }
-#pragma unroll
-        for (int u = 0; u < GR; ++u) {
-          const int m = m0 + u % LG * LP, eight = eight0 + u / LG * LG;
-          uint8_t* dst = smem + lay.terms + vr.slot * 6 * kTile * rp + ((m >> 3) * (3 * GR) + eight) * 128 + (m & 7) * 16;
-#pragma unroll
-          for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * GR * 128) = t[u][q];
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&v_full[vr.slot]);
-        vr.next();
-        if (k + 1 < count) wk.next();
-      }
-    }
+    make_terms(warp - 2);
   } else if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
-    // ---------------------------- rows that TMA does not bring, or not alone
+    // -------------------------------------------- mapped rows, or v's terms
     const int w4 = warp - kLoadWarp;
-    if (p.row) {
+    if (!p.row) {
+      make_terms(4 + w4);
+    } else {
       // A warp copies 32 rows of the tile, two at a time, and tells of a stage
       // when the copies of the stages after it are under way too.
       const int m0 = w4 * 32, hi = lane >> 4, piece = lane & 15;  // 16 bytes of a row's 256
@@ -507,8 +519,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       }
       cp_async_wait_all();
       while (pending) tell();
-    } else if (GRAD) {
-      // zeros behind a group's last row, up to the MMA's next step of 16
+    }
+  } else if (warp == kZeroWarp) {
+    // ------- zeros behind a group's last row, up to the MMA's next step of 16
+    if (GRAD && !p.row) {
       Ring st(p.stages);
       bool aborted = false;
       for (int64_t k = 0; k < count && !aborted; ++k) {
@@ -519,11 +533,12 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
             aborted = true;
             break;
           }
-          uint8_t* z = smem + st.slot * lay.stage + (lane >> 3 & 1) * kBox + (lane & 7) * 16;
-          for (int m = n + 2 * w4 + (lane >> 4); m < rows; m += 2 * kLoadWarps)
-            *reinterpret_cast<uint4*>(z + m * 128) = make_uint4(0, 0, 0, 0);
-          if (n < rows) fence_proxy_async_smem();
-          __syncwarp();
+          if (n < rows) {
+            uint8_t* z = smem + st.slot * lay.stage + (lane >> 3 & 1) * kBox + (lane & 7) * 16;
+            for (int m = n + (lane >> 4); m < rows; m += 2) *reinterpret_cast<uint4*>(z + m * 128) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           if (lane == 0) mbar_arrive(&loaded[st.slot]);
         }
         if (k + 1 < count) wk.next();
