@@ -198,7 +198,8 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // ------------------------------------------------ expansions: y and dx
 // out_i = base_i + (w v[p]) W over C columns: W is B_g [C, r] with v = s, w =
 // w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. Persistent CTAs walk
-// equal runs of the list of (columns of eight warps, tile of 128 positions). A
+// equal runs of the list of (columns of eight warps, tile of 16 to 128
+// positions). A
 // warp owns two strips of 32 columns (adjacent, or a gate and an up strip), keeps
 // its columns of W in registers while the group lasts, and takes a tile's
 // positions 16 at a time, the rows of base of the next kAhead sixteens under way,
@@ -206,7 +207,10 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // memory: no barrier). v's fragments (hi and lo terms, in the order of the MMA's
 // A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
 // strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
-// are eight consecutive columns: one 16-byte access to base, y and h.
+// are eight consecutive columns: one 16-byte access to base, y and h. 8192 rows
+// of 28672 columns, rank 16: 165 us (5.7 TB/s); dx of 4096 columns 21 us; 65536
+// rows of 2 x 768 columns, rank 32, with the activation: about 85 us (3.6 TB/s),
+// there bound by the issue and latency of 16 warps an SM.
 struct Expand {
   const uint16_t* w;
   bool scaled;
@@ -222,6 +226,7 @@ struct Expand {
   bool beside;     // nothing comes from the launch before this one but its own earlier work
   float* v_out;    // the slices' sum, written by the first columns' CTAs; or null
   int col_blocks;
+  AnyTile tile;
   float alpha, limit;
 };
 
@@ -296,12 +301,12 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
     return GLU == kGluHalves ? st * half + c : c + 32 * st;
   };
 
-  const Run run = find_run<kThreads>(d.offsets, d.G, d.R_max, e.col_blocks, s_sum, s_start);
+  const Run run = find_run<kThreads>(d.offsets, d.G, d.R_max, e.col_blocks, e.tile, s_sum, s_start);
   if (run.count == 0) {
     grid_dependency_wait();  // the grid must not complete before the launch it depends on
     return;
   }
-  Walk wk(d.offsets, d.G, d.R_max, run, s_start);  // thread 0's: the item after the next
+  Walk<AnyTile> wk(d.offsets, d.G, d.R_max, run, e.tile, s_start);  // thread 0's: the item after the next
   auto note = [&](int64_t k) {
     items[k % 3] = Item{wk.g, wk.cb, int32_t(wk.row0()), wk.n()};
     if (k + 1 < run.count) wk.next();
@@ -575,14 +580,19 @@ ContractArgs contract_of(const e4b_lora_args& a, const uint16_t* z, int64_t ld_z
   return c;
 }
 
-// s of a forward pass on the 128-row tiles of the tensor-core pass, or by
-// warps that split K where there are few rows (a decode batch).
-bool forward_uses_tiles(int64_t R_max) { return R_max > 512; }
+// s of a forward pass on the 128-row tiles of the tensor-core pass, or by warps
+// that split K where there is little to do (a decode batch). Whole calls, y
+// included, with one group and with 16, tiles against warps: rank 16, K = N =
+// 4096, 512 rows 13.2 and 13.5 against 9.6 and 9.8 us, 2048 rows 19.2 and 16.7
+// against 16.2 and 18.1; rank 64, 512 rows 22.1 and 16.7 against 20.8 and 19.5,
+// 2048 rows 32.0 and 27.5 against 36.7 and 44.9; K = N = 1024, 2048 rows, rank 16
+// 12.2 and 11.8 against 8.7 and 9.1, rank 64 21.3 and 19.7 against 18.9 and 21.5.
+bool forward_uses_tiles(int64_t R_max, int64_t K, int r) { return double(R_max) * double(K) * r > 2e8; }
 
 // Parts of s. Few rows: enough CTAs to fill the GPU, each with at least one
 // 32-wide chunk a warp.
 int forward_slices(int G, int r, int64_t K, int64_t R_max, int sms) {
-  if (forward_uses_tiles(R_max)) return contract_blocks(G, r, K, R_max, true, false, sms);
+  if (forward_uses_tiles(R_max, K, r)) return contract_blocks(G, r, K, R_max, true, false, sms);
   const int64_t tiles = pieces_bound(G, R_max, kShrinkRows);
   const int64_t most = (K + 32 * kWarps - 1) / (32 * kWarps);
   int64_t want = sms / (tiles > 0 ? tiles : 1);
@@ -596,8 +606,13 @@ cudaError_t launch_expand_of(const Adapters& d, Expand e, cudaStream_t st, int s
   constexpr int strips = kStrips<KS, GLU>;
   const int64_t cols = GLU == kGluHalves ? e.C / 2 : e.C, per = kWarps * (GLU == kGluHalves ? 32 : 32 * strips);
   e.col_blocks = int((cols + per - 1) / per);
-  int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, kTile);
-  if (grid > int64_t(sms) * kExpandCtas<KS, GLU>) grid = int64_t(sms) * kExpandCtas<KS, GLU>;
+  // the largest tile (a sixteen's MMAs need its factors staged) of which there are
+  // enough to go round: 128 rows of one group, r 64, 4096 columns took 19 us less so
+  const int64_t ctas = int64_t(sms) * kExpandCtas<KS, GLU>, groups = d.G < d.R_max ? d.G : d.R_max;
+  e.tile.bits = 7;
+  while (e.tile.bits > 4 && e.col_blocks * ((d.R_max >> e.tile.bits) + (groups + 1) / 2) < ctas) --e.tile.bits;
+  int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, int64_t(1) << e.tile.bits);
+  if (grid > ctas) grid = ctas;
   auto kernel = expand_kernel<KS, GLU, ACT, WT>;
   constexpr int staged = 2 * kSixteens * KS * 64 * 16, ring = (kAhead + 1) * 2 * strips * kThreads * 16;
   const int smem = staged + (e.base ? ring : 0);
@@ -663,7 +678,7 @@ cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaSt
   const int slices = forward_slices(a.G, a.r, a.K, a.R_max, sms);
   float* s = a.s && slices == 1 ? a.s : static_cast<float*>(ws);
   cudaError_t err;
-  if (forward_uses_tiles(a.R_max)) {
+  if (forward_uses_tiles(a.R_max, a.K, a.r)) {
     ContractArgs c = contract_of(a, a.x, a.ld_x, a.K, flags);
     c.w = a.a;
     c.out = s;
@@ -681,7 +696,7 @@ cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaSt
   if (!a.y && !a.h && slices == 1) return cudaSuccess;  // s alone was asked for
   const bool rows = a.y || a.h;  // else only s' parts are to be added
   const Expand e{a.b, true, a.N, rows ? a.base : nullptr, a.ld_base, a.y, a.ld_y, a.h, a.ld_h, s, slices, false,
-                 slices > 1 ? a.s : nullptr, 0, a.glu_alpha, a.glu_limit};
+                 slices > 1 ? a.s : nullptr, 0, AnyTile{}, a.glu_alpha, a.glu_limit};
   *launches = 2;
   return launch_expand(d, e, a.gate_up_layout, a.activation, st, sms);
 }
@@ -736,7 +751,7 @@ cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flag
     }
     if (a.dx) {
       const Expand e{a.a, false, a.K, a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, nullptr, 0, t, 1,
-                     a.da != nullptr, nullptr, 0, 0.f, 0.f};  // da's pass has waited for t and does not write it
+                     a.da != nullptr, nullptr, 0, AnyTile{}, 0.f, 0.f};  // da's pass has waited for t and does not write it
       if ((err = launch_expand_as<kGluNone, 0, true>(d, e, st, sms)) != cudaSuccess) return err;
       ++*launches;
     }

@@ -1,6 +1,6 @@
 // How the adapters' kernels share out their work: the list of (column block, row
-// tile), row tiles of 128 positions in group order, is cut into equal runs for
-// the CTAs, so that the groups' sizes do not unbalance it.
+// tile), row tiles of up to 128 positions in group order, is cut into equal runs
+// for the CTAs, so that the groups' sizes do not unbalance it.
 #pragma once
 
 #include <cstdint>
@@ -9,14 +9,25 @@
 
 namespace e4b {
 
-constexpr int kTile = 128;  // positions of a row tile
+constexpr int kTile = 128;  // positions of a row tile, at most
 
-__host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, int64_t R_max, int64_t& beg, int64_t& end) {
+// Positions of a row tile: 128, or another power of two.
+struct FullTile {
+  __host__ __device__ int shift() const { return 7; }
+};
+struct AnyTile {
+  int bits;
+  __host__ __device__ int shift() const { return bits; }
+};
+
+template <typename Size>
+__host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, int64_t R_max, int64_t& beg, int64_t& end,
+                                               Size size) {
   beg = offsets[g];
   end = offsets[g + 1];
   beg = beg < 0 ? 0 : beg > R_max ? R_max : beg;  // no position outside [0, R_max) is ever formed
   end = end < 0 ? 0 : end > R_max ? R_max : end;
-  return end > beg ? (end - beg + kTile - 1) / kTile : 0;
+  return end > beg ? (end - beg + (1 << size.shift()) - 1) >> size.shift() : 0;
 }
 
 // First item of CTA b's run out of W items over n CTAs.
@@ -31,13 +42,14 @@ struct Run {
 // By the whole CTA (ends with a barrier): the row tiles of all groups are added
 // up, and start receives the group and the tile within it that the run begins
 // with. sums: [THREADS / 32]. count 0: nothing is left for this CTA.
-template <int THREADS>
-E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, int blocks, int64_t* sums, int64_t* start) {
+template <int THREADS, typename Size>
+E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, int blocks, Size size, int64_t* sums,
+                     int64_t* start) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int strip = (G + THREADS - 1) / THREADS;
   const int lo = min(tid * strip, G), hi = min(lo + strip, G);
   int64_t beg, end, mine = 0;
-  for (int g = lo; g < hi; ++g) mine += group_tiles(offsets, g, R_max, beg, end);
+  for (int g = lo; g < hi; ++g) mine += group_tiles(offsets, g, R_max, beg, end, size);
   int64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -60,7 +72,7 @@ E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, 
   if (first >= before && first < before + mine) {
     int64_t left = first - before;
     for (int g = lo; g < hi; ++g) {
-      const int64_t t = group_tiles(offsets, g, R_max, beg, end);
+      const int64_t t = group_tiles(offsets, g, R_max, beg, end, size);
       if (left < t) {
         start[0] = g;
         start[1] = left;
@@ -74,19 +86,21 @@ E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, 
 }
 
 // A position in the list of (column block, row tile), row tiles in group order.
+template <typename Size>
 struct Walk {
   const int64_t* offsets;
   int64_t R_max, beg, end, tiles;
   int64_t tile;  // within the group
   int G, g, cb;
+  Size size;
 
-  E4B_DEV Walk(const int64_t* offs, int groups, int64_t r_max, const Run& run, const int64_t* start)
-      : offsets(offs), R_max(r_max), tile(start[1]), G(groups), cb(run.block) {
+  E4B_DEV Walk(const int64_t* offs, int groups, int64_t r_max, const Run& run, Size tile_size, const int64_t* start)
+      : offsets(offs), R_max(r_max), tile(start[1]), G(groups), cb(run.block), size(tile_size) {
     enter(int(start[0]));
   }
   E4B_DEV void enter(int group) {
     g = group;
-    tiles = group_tiles(offsets, g, R_max, beg, end);
+    tiles = group_tiles(offsets, g, R_max, beg, end, size);
   }
   E4B_DEV void next() {
     if (++tile < tiles) return;
@@ -98,8 +112,8 @@ struct Walk {
   }
   E4B_DEV bool first() const { return tile == 0; }
   E4B_DEV bool last() const { return tile + 1 == tiles; }
-  E4B_DEV int64_t row0() const { return beg + tile * kTile; }
-  E4B_DEV int n() const { return int(end - row0() < kTile ? end - row0() : kTile); }
+  E4B_DEV int64_t row0() const { return beg + (tile << size.shift()); }
+  E4B_DEV int n() const { return int(min(end - row0(), int64_t(1) << size.shift())); }
 };
 
 }  // namespace e4b

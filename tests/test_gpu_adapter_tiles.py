@@ -125,6 +125,13 @@ TILES = [  # counts, r, K, N, mapped
     ([5000], 16, 64, 64, False),                    # a group over all CTAs
     ([9000, 0, 3000], 64, 200, 136, True),
 ]
+WIDE = [  # enough work for s to run on tiles
+    ([6000, 131], 16, 2312, 72, True),
+    ([700] * 9 + [0, 1, 259], 24, 2048, 144, False),
+    ([2100, 900], 64, 1096, 328, False),
+    ([130] * 30, 48, 1160, 64, True),
+    ([12345], 8, 2056, 16, False),
+]
 
 
 @pytest.mark.parametrize("case", TILES, ids=str)
@@ -134,6 +141,29 @@ def test_tiles_forward_and_backward(case):
     s = c.s()
     c.check_backward(s, c.backward(s))
     assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: f"{len(c[0])} groups {c[1:]}")
+def test_wide_rows_forward_and_backward(case):
+    c = Case(*case, seed=11)
+    assert c.R * c.K * c.r > 2e8
+    c.check_forward(c.forward())
+    s = c.s()
+    c.check_backward(s, c.backward(s))
+    assert int(c.status) == 0
+
+
+ROWS = [(1, 1), (15, 2), (17, 1), (64, 3), (100, 1), (200, 2), (500, 1), (1500, 3)]
+
+
+@pytest.mark.parametrize("r", [8, 16, 32, 64])
+@pytest.mark.parametrize("rows,G", ROWS)
+def test_few_rows_take_smaller_tiles(rows, G, r):
+    # one long group and short ones, so that tiles of every size end inside a group
+    c = Case([rows] + [rows // 7 + 1] * (G - 1), r, 264, 520, seed=12)
+    c.check_forward(c.forward())
+    s = c.s()
+    c.check_backward(s, c.backward(s))
 
 
 @pytest.mark.parametrize("case", [TILES[1], TILES[4], TILES[9]], ids=str)
@@ -176,7 +206,7 @@ def test_values_of_other_groups_do_not_meet():
 
 
 def test_a_wait_that_gives_up_is_reported_and_the_next_call_works():
-    c = Case([600, 300], 16, 256, 512, seed=4)
+    c = Case([6000, 2300], 16, 2048, 512, seed=4)  # s on tiles too
     s = c.s()
     c.forward(flags=e4b.FLAG_TEST_TIMEOUT)
     first = int(c.status)
