@@ -730,6 +730,7 @@ cudaError_t launch_lora_backward(const e4b_lora_args& a, void* ws, uint32_t flag
   if (parts == 1) t = y.out;
   ContractArgs x = contract_of(a, a.x, a.ld_x, a.K, flags);
   if (a.da) {
+    x.follows = true;
     x.v = t;
     x.grad = a.da;
     x.accumulate = accumulate;

@@ -97,7 +97,7 @@ struct Pass {
   int blocks, chunks;  // column blocks; column tiles of a block
   int stages, vbufs;
   uint32_t limit;
-  uint8_t w_t, scale_out, scale_v, grad_t, accumulate;
+  uint8_t w_t, scale_out, scale_v, grad_t, accumulate, follows;
 };
 
 // Shared memory, from a 1024-byte boundary: stages of (tile, W's box), the
@@ -203,13 +203,21 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  if (GRAD && tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
+  if (tid == 0) {
+    prefetch_tensormap(&tm_tile);
+    prefetch_tensormap(&tm_edge);
+    if (OUT) prefetch_tensormap(&tm_w);
+  }
+  // offsets do not come from the launch before this one where that is a part of
+  // the same call, which has itself waited for all earlier work
+  if (!p.follows) grid_dependency_wait();
   const Run run = find_run<kThreads>(p.offsets, p.G, p.R_max, p.blocks, FullTile{}, s_sum, s_start);
-  if (run.count == 0) return;  // uniform
   const int64_t count = run.count;
+  if (count == 0) {  // uniform
+    if (p.follows) grid_dependency_wait();
+    if (GRAD && tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
+    return;
+  }
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -237,6 +245,13 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  if (p.follows) grid_dependency_wait();
+  grid_launch_dependents();
+  if (GRAD) {
+    // the results' warps note the parts, behind this barrier
+    if (tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
+    __syncthreads();
+  }
 
   const int all_chunks = int((p.C + kTile - 1) / kTile);
   constexpr int rp = RP;
@@ -859,6 +874,7 @@ Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   p.scale_v = a.scale_v;
   p.grad_t = a.grad_t;
   p.accumulate = a.accumulate;
+  p.follows = a.follows;
   return p;
 }
 

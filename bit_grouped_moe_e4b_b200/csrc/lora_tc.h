@@ -34,6 +34,7 @@ struct ContractArgs {
   bool accumulate;     // add to grad
   float* grad_part;    // contract_part_bytes
 
+  bool follows;        // the launch before it on the stream belongs to the same call
   int32_t* status;     // or null
   bool no_wait;        // waits give up at once (tests)
 };

@@ -113,6 +113,8 @@ E4B_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar
 E4B_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------ TMA
+E4B_DEV void prefetch_tensormap(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
+
 E4B_DEV void tma_load_2d(void* dst, const void* tmap, uint64_t* bar, int32_t x, int32_t y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
