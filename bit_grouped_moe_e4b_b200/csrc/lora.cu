@@ -293,13 +293,15 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   __shared__ int64_t s_sum[kWarps], s_start[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q = lane & 3, rr = lane >> 2;
-  const int64_t half = e.C / 2;
-  const int64_t limit[2] = {GLU == kGluHalves ? half : e.C, e.C};
+  const int C = int(e.C), half = C / 2;
+  const int limit[2] = {GLU == kGluHalves ? half : C, C};
   // first columns of the warp's strips
   auto strip = [&](int cb, int st) {
-    const int64_t c = (int64_t(cb) * kWarps + warp) * (GLU == kGluHalves ? 32 : 32 * ST);
+    const int c = (cb * kWarps + warp) * (GLU == kGluHalves ? 32 : 32 * ST);
     return GLU == kGluHalves ? st * half + c : c + 32 * st;
   };
+  // a row's place: rows count from 0
+  auto place = [](int32_t row, int64_t ld) { return uint64_t(uint32_t(row)) * uint64_t(ld); };
 
   const Run run = find_run<kThreads>(d.offsets, d.G, d.R_max, e.col_blocks, e.tile, s_sum, s_start);
   if (run.count == 0) {
@@ -323,7 +325,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
 #pragma unroll
     for (int st = 0; st < ST; ++st) {
       if constexpr (WT) {
-        const int64_t n = strip(t.cb, st) + 8 * (rr >> 1);
+        const int n = strip(t.cb, st) + 8 * (rr >> 1);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const int j = 16 * ks + 4 * q;
@@ -341,12 +343,12 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int64_t n = strip(t.cb, st) + 8 * (rr >> 1) + 2 * i + (rr & 1);
+          const int n = strip(t.cb, st) + 8 * (rr >> 1) + 2 * i + (rr & 1);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             const int j = 16 * ks + 4 * q;
             uint2 v = make_uint2(0, 0);
-            if (n < limit[st] && j < d.r) v = __ldg(reinterpret_cast<const uint2*>(wg + n * d.r + j));
+            if (n < limit[st] && j < d.r) v = __ldg(reinterpret_cast<const uint2*>(wg + int64_t(n) * d.r + j));
             bf[st][i][ks][0] = v.x;
             bf[st][i][ks][1] = v.y;
           }
@@ -405,16 +407,29 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
 
   int asked = 0, taken = 0;  // sixteens of base: asked for, and used
   auto slot = [&](int k, int i, int st) { return ring + ((k % (kAhead + 1) * 2 + i) * ST + st) * kThreads + tid; };
-  auto fetch = [&](int buf, int six, int cb) {
+  // the lane's columns of an item
+  struct Columns {
+    int c[ST];
+    bool in[ST];
+  };
+  auto columns = [&](int cb) {
+    Columns k;
+#pragma unroll
+    for (int st = 0; st < ST; ++st) {
+      k.c[st] = strip(cb, st) + 8 * q;
+      k.in[st] = k.c[st] < limit[st];
+    }
+    return k;
+  };
+  auto fetch = [&](int buf, int six, const Columns& k) {
     if (e.base) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int32_t row = at[buf][16 * six + rr + 8 * i];
+        const uint16_t* from = e.base + place(row, e.ld_base);
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          const int64_t c = strip(cb, st) + 8 * q;
-          if (row >= 0 && c < limit[st]) sm100::cp_async_16(slot(asked, i, st), e.base + int64_t(row) * e.ld_base + c, 16);
-        }
+        for (int st = 0; st < ST; ++st)
+          if (row >= 0 && k.in[st]) sm100::cp_async_16(slot(asked, i, st), from + k.c[st], 16);
       }
     }
     sm100::cp_async_commit();
@@ -440,14 +455,8 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
     const int sixteens = (t.n + 15) / 16, next_sixteens = (next.n + 15) / 16;
     const int stage_at = sixteens > kAhead ? sixteens - kAhead : 0;  // from here on the next item's rows are asked for
     int next_had = 0;
-    while (had < sixteens && had < kAhead) fetch(buf, had++, t.cb);
-    int64_t c[ST];
-    bool in[ST];
-#pragma unroll
-    for (int st = 0; st < ST; ++st) {
-      c[st] = strip(t.cb, st) + 8 * q;
-      in[st] = c[st] < limit[st];
-    }
+    const Columns cols = columns(t.cb);
+    while (had < sixteens && had < kAhead) fetch(buf, had++, cols);
     for (int six = 0; six < sixteens; ++six) {
       if (more && six == stage_at) {
         __syncthreads();  // all warps are past the item that used these fragments
@@ -456,9 +465,9 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
         __syncthreads();
       }
       if (had < sixteens)
-        fetch(buf, had++, t.cb);
+        fetch(buf, had++, cols);
       else if (more && next_had < next_sixteens && next_had < kAhead)
-        fetch(buf ^ 1, next_had++, next.cb);
+        fetch(buf ^ 1, next_had++, next.cb == t.cb ? cols : columns(next.cb));
       arrived();
       int32_t row[2];
       float acc[ST][4][4];  // starts as base
@@ -467,7 +476,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
         row[i] = at[buf][16 * six + rr + 8 * i];
 #pragma unroll
         for (int st = 0; st < ST; ++st) {
-          const uint4 b = e.base && in[st] && row[i] >= 0 ? *slot(taken, i, st) : make_uint4(0, 0, 0, 0);
+          const uint4 b = e.base && cols.in[st] && row[i] >= 0 ? *slot(taken, i, st) : make_uint4(0, 0, 0, 0);
           const uint32_t words[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -499,21 +508,21 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
             v[st][2 * p] = acc[st][p][2 * i];
             v[st][2 * p + 1] = acc[st][p][2 * i + 1];
           }
-          if (e.y && in[st]) *reinterpret_cast<uint4*>(e.y + int64_t(row[i]) * e.ld_y + c[st]) = pack8(v[st]);
+          if (e.y && cols.in[st]) *reinterpret_cast<uint4*>(e.y + place(row[i], e.ld_y) + cols.c[st]) = pack8(v[st]);
         }
         if constexpr (GLU == kGluHalves) {
           float h[8];
 #pragma unroll
           for (int p = 0; p < 8; ++p) h[p] = activate<ACT>(v[0][p], v[1][p], e.alpha, e.limit);
-          if (in[0]) *reinterpret_cast<uint4*>(e.h + int64_t(row[i]) * e.ld_h + c[0]) = pack8(h);
+          if (cols.in[0]) *reinterpret_cast<uint4*>(e.h + place(row[i], e.ld_h) + cols.c[0]) = pack8(h);
         } else if constexpr (GLU == kGluInterleaved) {
 #pragma unroll
           for (int st = 0; st < ST; ++st) {
             float h[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p) h[p] = activate<ACT>(v[st][2 * p], v[st][2 * p + 1], e.alpha, e.limit);
-            if (in[st])
-              *reinterpret_cast<uint2*>(e.h + int64_t(row[i]) * e.ld_h + c[st] / 2) =
+            if (cols.in[st])
+              *reinterpret_cast<uint2*>(e.h + place(row[i], e.ld_h) + cols.c[st] / 2) =
                   make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
           }
         }

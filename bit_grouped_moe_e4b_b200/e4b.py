@@ -484,6 +484,14 @@ def _matrix(name, t):
     return t.shape
 
 
+def _rows_wide(name, t, width, dev):
+    """(address, row stride, n) of bf16 rows [n, width] on device dev."""
+    n, w = _matrix(name, t)
+    if w != width:
+        _refuse(name, t, _BF16, (n, width), dev, True)
+    return *_same_rows(name, t, n, width, dev), n
+
+
 # the device of a process that has a CUDA tensor in hand
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
@@ -509,30 +517,27 @@ def _call(name, dev, stream, *args):
 
 def e4b_permute(x, perm, offsets, xs, *, top_k, stream=None):
     """xs[p] = x[perm[p] / top_k] for p < offsets[E] (x [T, H], xs [R_max, H])."""
-    T, H = _matrix("x", x)
-    R, dev = _matrix("xs", xs)[0], x.get_device()
+    (T, H), dev = _matrix("x", x), x.get_device()
+    to, ld, R = _rows_wide("xs", xs, H, dev)
     if R > T * top_k:
         raise ValueError("xs has more rows than there are slots")
     E = offsets.numel() - 1
-    _call("e4b_permute", dev, stream, *_same_rows("x", x, T, H, dev), T, H,
-          _vec1("perm", perm, _I32, T * top_k, dev), top_k, _vec1("offsets", offsets, _I64, E + 1, dev), E, R,
-          *_rows("xs", xs, R, H, dev))
+    _call("e4b_permute", dev, stream, *_same_rows("x", x, T, H, dev), T, H, _vec1("perm", perm, _I32, T * top_k, dev),
+          top_k, _vec1("offsets", offsets, _I64, E + 1, dev), E, R, to, ld)
 
 
 def e4b_permute_backward(dxs, inv_perm, dx, *, top_k, stream=None):
     """dx[t] = the sum of its slots' rows of dxs (dxs [R_max, H], dx [T, H])."""
-    T, H = _matrix("dx", dx)
-    R, dev = _matrix("dxs", dxs)[0], dx.get_device()
-    _call("e4b_permute_backward", dev, stream, *_rows("dxs", dxs, R, H, dev), R, H,
+    (T, H), dev = _matrix("dx", dx), dx.get_device()
+    _call("e4b_permute_backward", dev, stream, *_rows_wide("dxs", dxs, H, dev), H,
           _vec1("inv_perm", inv_perm, _I32, T * top_k, dev), T, top_k, *_same_rows("dx", dx, T, H, dev))
 
 
 def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
     """y[t] = the gate-weighted sum of its slots' rows of ys (ys [R_max, H],
     gates fp32 [T, top_k] or None, y [T, H])."""
-    T, H = _matrix("y", y)
-    R, dev = _matrix("ys", ys)[0], y.get_device()
-    _call("e4b_unpermute", dev, stream, *_rows("ys", ys, R, H, dev), R, H,
+    (T, H), dev = _matrix("y", y), y.get_device()
+    _call("e4b_unpermute", dev, stream, *_rows_wide("ys", ys, H, dev), H,
           _vec1("inv_perm", inv_perm, _I32, T * top_k, dev),
           None if gates is None else _vec("gates", gates, _F32, (T, top_k), dev), T, top_k,
           *_same_rows("y", y, T, H, dev))
@@ -541,8 +546,7 @@ def e4b_unpermute(ys, inv_perm, gates, y, *, top_k, stream=None):
 def e4b_unpermute_backward(dy, ys, inv_perm, gates, dys, dgates, *, top_k, stream=None):
     """dys[inv_perm[s]] = gates[s] dy[t] and dgates[s] = <dy[t], ys[inv_perm[s]]>;
     dys or dgates may be None, and ys where dgates is."""
-    T, H = _matrix("dy", dy)
-    dev = dy.get_device()
+    (T, H), dev = _matrix("dy", dy), dy.get_device()
     if (ys is None and dys is None) or (ys is None and dgates is not None) or (dys is None and dgates is None):
         raise ValueError("ys is needed for dgates, dys or dgates for a result")
     R = _matrix("ys", dys if ys is None else ys)[0]
