@@ -204,8 +204,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    prefetch_tensormap(&tm_tile);
-    prefetch_tensormap(&tm_edge);
+    if (!p.row) {
+      prefetch_tensormap(&tm_tile);
+      prefetch_tensormap(&tm_edge);
+    }
     if (OUT) prefetch_tensormap(&tm_w);
   }
   // offsets do not come from the launch before this one where that is a part of
@@ -909,11 +911,14 @@ size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int
 cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
   const Plan q = plan_of(a.G, a.r, a.C, a.R_max, a.out != nullptr, a.grad != nullptr, sms);
   const Pass p = pass_of(a, q, sms);
-  CUtensorMap tile, edge, w;
-  bool ok = encode_2d(&tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
-                      64, kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
-            encode_2d(&edge, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2,
-                      64, kEdge, CU_TENSOR_MAP_SWIZZLE_128B);
+  CUtensorMap tile{}, edge{}, w{};
+  bool ok = true;
+  if (!a.row) {  // mapped rows do not come by TMA
+    ok = encode_2d(&tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2, 64,
+                   kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_2d(&edge, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z, uint64_t(a.C), uint64_t(p.rows), uint64_t(a.ld_z) * 2, 64,
+                   kEdge, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
   if (a.out) {
     // a group's matrix is a plane of its own, so that a box past its edge reads zeros
     const CUtensorMapSwizzle span = q.rp == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -922,8 +927,6 @@ cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {
     ok = ok && (a.w_t ? encode_planes(&w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.r, a.C, a.G, 2, q.rp, kTile, span)
                       : encode_planes(&w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.C, a.r, a.G, 2, 64, q.rp,
                                       CU_TENSOR_MAP_SWIZZLE_128B));
-  } else {
-    w = tile;
   }
   if (!ok) return cudaErrorInvalidValue;
   if (q.rp == 16) return launch_as<16>(a, tile, edge, w, p, st, sms);

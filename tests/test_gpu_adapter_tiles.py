@@ -271,3 +271,23 @@ def test_without_rows_gradients_are_zero_and_nothing_else_is_written():
     assert bool((out["dx"] == SENTINEL).all())
     fwd = c.forward()
     assert bool((fwd["y"] == SENTINEL).all()) and bool((fwd["s"] == SENTINEL).all())
+
+
+def test_a_map_without_any_row_in_range():
+    # every position is left out: s is zero, gradients are zero, no row is written
+    c = Case([200, 57], 16, 72, 136, mapped=True, seed=13)
+    c.row.fill_(-1)
+    c.used[:] = False
+    fwd = c.forward()
+    assert not bool(fwd["s"][:c.n].any()) and bool((fwd["y"] == SENTINEL).all())
+    out = c.backward(torch.ones(c.R, c.r, device="cuda"))
+    assert not bool(out["da"].any()) and not bool(out["db"].any()) and bool((out["dx"] == SENTINEL).all())
+
+
+def test_largest_group_count_and_single_positions():
+    # 1024 groups, most of them empty, the rest of one position
+    counts = [1 if g % 7 == 3 else 0 for g in range(1024)]
+    c = Case(counts, 8, 40, 24, seed=14)
+    c.check_forward(c.forward())
+    s = c.s()
+    c.check_backward(s, c.backward(s))
