@@ -30,8 +30,11 @@ __host__ __device__ inline int64_t group_tiles(const int64_t* offsets, int g, in
   return end > beg ? (end - beg + (1 << size.shift()) - 1) >> size.shift() : 0;
 }
 
-// First item of CTA b's run out of W items over n CTAs.
-__host__ __device__ inline int64_t run_start(int64_t W, int64_t n, int64_t b) { return b * W / n; }
+// a / b for a >= 0, b > 0, in 32 bits where they fit: a kernel's start waits for
+// these divisions (in 64 bits they took a microsecond).
+E4B_DEV int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 
 // A CTA's run: the column block it begins in, and its items.
 struct Run {
@@ -63,11 +66,12 @@ E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, 
     if (w < warp) before += sums[w];
     T += sums[w];
   }
-  const int64_t W = T * blocks;
-  const int64_t ctas = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
-  if (int64_t(blockIdx.x) >= ctas) return Run{0, 0};  // uniform; also where no group has rows
-  const int64_t w0 = run_start(W, ctas, blockIdx.x);
-  const int block = int(w0 / T);
+  const int64_t W = T * blocks, b = blockIdx.x;
+  if (b >= W) return Run{0, 0};  // uniform; also where no group has rows
+  // the first `longer` runs have an item more
+  const int64_t length = quotient(W, gridDim.x), longer = W - length * gridDim.x;
+  const int64_t w0 = b * length + min(b, longer), count = length + (b < longer);
+  const int block = int(quotient(w0, T));
   const int64_t first = w0 - block * T;
   if (first >= before && first < before + mine) {
     int64_t left = first - before;
@@ -82,7 +86,7 @@ E4B_DEV Run find_run(const int64_t* __restrict__ offsets, int G, int64_t R_max, 
     }
   }
   __syncthreads();
-  return Run{block, run_start(W, ctas, int64_t(blockIdx.x) + 1) - w0};
+  return Run{block, count};
 }
 
 // A position in the list of (column block, row tile), row tiles in group order.
