@@ -63,6 +63,7 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kLoadWarp = 10, kLoadWarps = 4, kGradWarp = 14, kZeroWarp = 15;
+constexpr int kNoteThread = 8 * 32;              // of the results' warps, writes the CTA's notes
 static_assert(kTile == 128, "positions, and columns, of an operand tile");
 constexpr uint32_t kBox = kTile * 128;           // bytes of 128 rows of 64 columns
 constexpr int kEdge = 32;                        // rows of the boxes at a group's end
@@ -209,18 +210,6 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
       prefetch_tensormap(&tm_edge);
     }
     if (OUT) prefetch_tensormap(&tm_w);
-  }
-  // offsets do not come from the launch before this one where that is a part of
-  // the same call, which has itself waited for all earlier work
-  if (!p.follows) grid_dependency_wait();
-  const Run run = find_run<kThreads>(p.offsets, p.G, p.R_max, p.blocks, FullTile{}, s_sum, s_start);
-  const int64_t count = run.count;
-  if (count == 0) {  // uniform
-    if (p.follows) grid_dependency_wait();
-    if (GRAD && tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
-    return;
-  }
-  if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&loaded[s], p.row ? kLoadWarps : 1);
@@ -244,15 +233,19 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  // offsets do not come from the launch before this one where that is a part of
+  // the same call, which has itself waited for all earlier work
+  if (!p.follows) grid_dependency_wait();
+  const Run run = find_run<kThreads>(p.offsets, p.G, p.R_max, p.blocks, FullTile{}, s_sum, s_start);  // has barriers
   if (p.follows) grid_dependency_wait();
   grid_launch_dependents();
-  if (GRAD) {
-    // the results' warps note the parts, behind this barrier
-    if (tid < 2) p.notes[2 * blockIdx.x + tid] = Note{-1, 0, 0};
-    __syncthreads();
+  if (GRAD && tid == kNoteThread) p.notes[2 * blockIdx.x] = p.notes[2 * blockIdx.x + 1] = Note{-1, 0, 0};
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int64_t count = run.count;
+  if (count == 0) {  // uniform
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
   }
 
   const int all_chunks = int((p.C + kTile - 1) / kTile);
@@ -610,7 +603,7 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
           direct = wk.first() && wk.tiles <= count - k;
           later = false;
           part = 2 * int(blockIdx.x) + (k ? 1 : 0);
-          if (!direct && m == 0) p.notes[part] = Note{wk.g, wk.cb, wk.first()};
+          if (!direct && tid == kNoteThread) p.notes[part] = Note{wk.g, wk.cb, wk.first()};
         }
         const bool fresh = ++chain == kGradChain || wk.last();
         if (fresh || k + 1 == count) {
