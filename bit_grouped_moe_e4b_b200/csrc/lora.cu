@@ -208,7 +208,7 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
 // strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
 // are eight consecutive columns: one 16-byte access to base, y and h. 8192 rows
-// of 28672 columns, rank 16: 165 us (5.7 TB/s); dx of 4096 columns 21 us; 65536
+// of 28672 columns, rank 16: 161 us (5.8 TB/s); dx of 4096 columns 21 us; 65536
 // rows of 2 x 768 columns, rank 32, with the activation: about 85 us (3.6 TB/s),
 // there bound by the issue and latency of 16 warps an SM.
 struct Expand {
@@ -230,7 +230,8 @@ struct Expand {
   float alpha, limit;
 };
 
-constexpr int kAhead = 3;  // sixteens of base under way
+constexpr int kAhead = 2;  // sixteens of base under way (one or three: 2 to 4 us more for 8192 rows of 28672)
+static_assert(kAhead == 2, "expand_kernel waits for at most two later ones");
 constexpr int kSixteens = kTile / 16;
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
@@ -437,8 +438,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   };
   auto arrived = [&]() {  // the oldest sixteen
     const int later = asked - taken - 1;
-    if (later >= 3) sm100::cp_async_wait<3>();
-    else if (later == 2) sm100::cp_async_wait<2>();
+    if (later >= 2) sm100::cp_async_wait<2>();
     else if (later == 1) sm100::cp_async_wait<1>();
     else sm100::cp_async_wait<0>();
   };

@@ -714,9 +714,10 @@ E4B_DEV void finish_parts(const Finish& f, int b) {
   const Pass& p = f.p;
   __shared__ int s_last;
   const int64_t block = int64_t(p.chunks) * kTile, part = block * p.r;
+  const Note notes[2] = {p.notes[2 * b], p.notes[2 * b + 1]};
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    const Note note = p.notes[2 * b + k];
+    const Note note = k ? notes[1] : notes[0];
     if (note.group < 0 || !note.first) continue;  // uniform
     __syncthreads();
     if (threadIdx.x == 0) s_last = f.ctas - 1;
@@ -764,13 +765,12 @@ E4B_DEV void finish_parts(const Finish& f, int b) {
 E4B_DEV void finish_empty(const Pass& p, int g) {
   const int64_t n4 = p.C * p.r / 4;
   float4* dst = reinterpret_cast<float4*>(p.grad) + int64_t(g) * n4;
-  const int64_t cta = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, ctas = int64_t(gridDim.x) * gridDim.y;
-  for (int64_t i = cta * kFinishThreads + threadIdx.x; i < n4; i += ctas * kFinishThreads)
+  for (int64_t i = int64_t(blockIdx.x) * kFinishThreads + threadIdx.x; i < n4; i += int64_t(gridDim.x) * kFinishThreads)
     dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// CTAs (x, y): piece y of the first pass' parts, then of the second's; all of them
-// share the groups without rows.
+// CTAs (x, y): piece y of the first pass' parts, then of the second's; those of the
+// first pieces share the groups without rows.
 __global__ void __launch_bounds__(kFinishThreads)
 finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b) {
   grid_dependency_wait();
@@ -778,7 +778,7 @@ finish_kernel(const __grid_constant__ Finish a, const __grid_constant__ Finish b
   const int x = blockIdx.x;
   if (x < a.ctas) finish_parts(a, x);
   else if (x < a.ctas + b.ctas) finish_parts(b, x - a.ctas);
-  if (a.p.accumulate) return;
+  if (a.p.accumulate || blockIdx.y) return;
   const Pass& p = a.p;
   __shared__ uint32_t s_empty[kFinishThreads / 32];
   for (int g0 = 0; g0 < p.G; g0 += kFinishThreads) {
