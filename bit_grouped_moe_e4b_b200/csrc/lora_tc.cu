@@ -820,7 +820,8 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   if (tiles < groups) tiles = groups;
   double best = 0;
   q.chunks = 0;
-  for (int64_t c = 1; c <= most && c <= all; ++c) {
+  // without a gradient up to 64 tiles, in steps that grow: this runs on the host for every call
+  for (int64_t c = 1; c <= most && c <= all; c += grad || c < 4 ? 1 : c < 16 ? 4 : 16) {
     const int64_t blocks = (all + c - 1) / c, items = blocks * tiles;
     double t = double((items + sms - 1) / sms) * (double(c) + (grad && q.rp == 64 ? 1.5 : 0.5));
     if (grad) t += 0.5 * double(c);

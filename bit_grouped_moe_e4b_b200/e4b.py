@@ -444,7 +444,14 @@ def _refuse(name, t, dtype, shape, dev, rows):
 
 def _vec(name, t, dtype, shape, dev):
     """The address of a contiguous tensor of this type and shape on device dev."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+    if t.shape != shape:
+        _refuse(name, t, dtype, shape, dev, False)
+    return _same_vec(name, t, dtype, shape, dev)
+
+
+def _same_vec(name, t, dtype, shape, dev):
+    """_vec of a tensor whose shape is known to be `shape`."""
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev or dev < 0:
         _refuse(name, t, dtype, shape, dev, False)
     return t.data_ptr()
 
@@ -602,10 +609,13 @@ def _lora_args(a, b, offsets, scale, row, n, dev):
     """The arguments both directions share; n: rows that positions point into."""
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a: expected [G, r, K], b: expected [G, N, r]")
-    G, r, K = a.shape
-    N = b.shape[1]
+    sa, sb = a.shape, b.shape
+    G, r, K = sa
+    N = sb[1]
+    if sb != (G, N, r):
+        _refuse("b", b, _BF16, (G, N, r), dev, False)
     R_max = n if row is None else row.numel()
-    return LoraArgs(G, r, N, K, R_max, _vec("a", a, _BF16, (G, r, K), dev), _vec("b", b, _BF16, (G, N, r), dev),
+    return LoraArgs(G, r, N, K, R_max, _same_vec("a", a, _BF16, sa, dev), _same_vec("b", b, _BF16, sb, dev),
                     None if scale is None else _vec1("scale", scale, _F32, G, dev),
                     _vec1("offsets", offsets, _I64, G + 1, dev),
                     None if row is None else _vec1("row", row, _I32, R_max, dev), n)
