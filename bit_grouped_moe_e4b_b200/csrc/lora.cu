@@ -199,12 +199,11 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // out_i = base_i + (w v[p]) W over C columns: W is B_g [C, r] with v = s, w =
 // w_g, or A_g [r, C] transposed (WT) with v = t, w = 1. Persistent CTAs walk
 // equal runs of the list of (columns of eight warps, tile of 16 to 128
-// positions). A
-// warp owns two strips of 32 columns (adjacent, or a gate and an up strip), keeps
-// its columns of W in registers while the group lasts, and takes a tile's
-// positions 16 at a time, the rows of base of the next kAhead sixteens under way,
-// past the end of the tile too (cp.async into the lane's own slots of shared
-// memory: no barrier). v's fragments (hi and lo terms, in the order of the MMA's
+// positions). A warp owns two strips of 32 columns (adjacent, or a gate and an up
+// strip), keeps its columns of W in registers while the group lasts, and takes a
+// tile's positions 16 at a time, the rows of base of the next kAhead sixteens
+// under way, past the end of the tile too (cp.async into the lane's own slots of
+// shared memory: no barrier). v's fragments (hi and lo terms, in the order of the MMA's
 // A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
 // strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
 // are eight consecutive columns: one 16-byte access to base, y and h. 8192 rows
@@ -236,10 +235,11 @@ constexpr int kSixteens = kTile / 16;
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
 
-// The activation of an expanded pair, in six instructions a value for SwiGLU:
-// exp2 and the reciprocal without their handling of denormals (which took 16,
-// and the kernel's time with them). Where the reciprocal flushes to zero the
-// exact factor is under 2^-125.
+// The activation of an expanded pair: exp2 and the reciprocal without their
+// handling of denormals, six instructions a value for SwiGLU instead of 16. Where
+// the reciprocal flushes to zero the exact factor is under 2^-125. The gate meets
+// its sigmoid before the up value, so that no product overflows on the way to a
+// finite result.
 template <int ACT>
 E4B_DEV float activate(float g, float u, float alpha, float limit) {
   if constexpr (ACT == E4B_ACT_CLAMPED_GLU) {
@@ -250,7 +250,7 @@ E4B_DEV float activate(float g, float u, float alpha, float limit) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (slope * -1.4426950408889634f)));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-  return (g * u) * s;
+  return (g * s) * u;
 }
 
 E4B_DEV uint4 pack8(const float (&a)[8]) {

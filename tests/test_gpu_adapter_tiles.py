@@ -291,3 +291,26 @@ def test_largest_group_count_and_single_positions():
     c.check_forward(c.forward())
     s = c.s()
     c.check_backward(s, c.backward(s))
+
+
+@pytest.mark.parametrize("layout", ["halves", "interleaved"])
+@pytest.mark.parametrize("act", ["swiglu", "clamped_glu"])
+def test_activation_of_huge_values_does_not_overflow_on_the_way(layout, act):
+    # a gate far below zero closes whatever the up value is; no adapter term (scale 0)
+    c = Case([40], 8, 16, 64, seed=15)
+    c.scale.zero_()
+    g = torch.tensor([-1e20, -300.0, -3e38, -100.0, 2.0, -1e3], device="cuda").to(BF16)
+    u = torch.tensor([1e20, 1e37, -3e38, 1e30, 3.0, 3e38], device="cuda").to(BF16)
+    reps = c.N // 2 // len(g) + 1
+    gu = ref.join_gu(g.repeat(reps)[None, :c.N // 2], u.repeat(reps)[None, :c.N // 2], layout)
+    c.base = gu.expand(c.rows, -1).contiguous()
+    h = c.full(c.rows, c.N // 2)
+    c.forward(h=h, layout=layout, act=act)
+    want = ref.glu(*ref.split_gu(gu, layout), act)[0].to(F32)
+    assert bool(torch.isfinite(want).all())
+    got = h[:c.n].to(F32)
+    assert bool(torch.isfinite(got).all())
+    # half a bf16 step and 2^-18 of the value; a sigmoid that the reciprocal flushes leaves 2^-124 of |g u'| at most
+    a, b = (v.double().abs() for v in ref.split_gu(gu, layout))
+    flushed = 2.0 ** -124 * a * (torch.clamp(b, max=7.0) + 1 if act == "clamped_glu" else b)
+    assert bool(((got - want).abs().double() <= (2 ** -8 + 2 ** -18) * want.abs().double() + flushed).all())
