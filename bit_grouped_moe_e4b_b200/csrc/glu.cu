@@ -113,7 +113,8 @@ struct GluVec {
         const float sg = fast_sigmoid(slope * gc);
         const float f = gc * sg;
         h[i] = f * uc;
-        dg[i] = gout ? 0.f : dw[i] * uc * (sg * fmaf(slope * gc, 1.f - sg, 1.f));
+        // sg (1 + a g' (1 - sg)) as sg + a (g' sg) (1 - sg): no factor overflows where the gate is closed
+        dg[i] = gout ? 0.f : dw[i] * (uc * fmaf(slope * f, 1.f - sg, sg));
         du[i] = uout ? 0.f : dw[i] * f;
       }
       uint16_t* dst = r.dgu + row * r.ld_dgu;

@@ -314,3 +314,25 @@ def test_activation_of_huge_values_does_not_overflow_on_the_way(layout, act):
     a, b = (v.double().abs() for v in ref.split_gu(gu, layout))
     flushed = 2.0 ** -124 * a * (torch.clamp(b, max=7.0) + 1 if act == "clamped_glu" else b)
     assert bool(((got - want).abs().double() <= (2 ** -8 + 2 ** -18) * want.abs().double() + flushed).all())
+
+
+@pytest.mark.parametrize("layout", ["halves", "interleaved"])
+@pytest.mark.parametrize("act", ["swiglu", "clamped_glu"])
+def test_activation_gradient_of_huge_values_does_not_overflow_on_the_way(layout, act):
+    g = torch.tensor([-1e20, -300.0, -3e38, -100.0, 2.0, -1e3, 5.0, -3e38], device="cuda").to(BF16)
+    u = torch.tensor([1e20, 1e37, -3e38, 1e30, 3.0, 3e38, -2.0, 0.0], device="cuda").to(BF16)
+    dh = torch.tensor([1e20, -1e30, 1e10, 2.0, 1.5, 3e38, -0.5, 3e38], device="cuda").to(BF16)
+    R = 9
+    gu = ref.join_gu(g[None], u[None], layout).expand(R, -1).contiguous()
+    d = dh.expand(R, -1).contiguous()
+    dgu, h = torch.empty_like(gu), torch.empty_like(d)
+    e4b.e4b_glu_backward(d, gu, dgu, h=h, layout=layout, act=act)
+    h_ref, dg, du = ref.glu(g.double()[None], u.double()[None], act)
+    open_ = (g.float() > -90)[None]  # elsewhere the gate is closed: nothing passes
+    got_g, got_u = ref.split_gu(dgu, layout)
+    for got, want in ((h, h_ref), (got_g, dg * dh.double()), (got_u, du * dh.double())):
+        assert bool(torch.isfinite(got.float()).all())
+        err = (got.double() - want).abs()
+        # half a bf16 step and 2^-16 for the gradient's few roundings
+        assert bool((err <= (2 ** -8 + 2 ** -16) * want.abs())[open_.expand_as(err)].all())
+        assert not bool(got[~open_.expand_as(err)].any())
