@@ -16,12 +16,14 @@
 // over the GPU count and 128-row tiles would be empty.
 //
 // Numbers: x, y, dy, A and B enter the MMAs as they are (bf16); sums are fp32.
-// The fp32 values s and t enter an expansion, whose result is rounded to bf16,
-// as two bf16 terms hi + lo (hi = bf16(v), lo = bf16(v - hi)): 16 bits and more
-// of mantissa. All reductions run in an order that depends on the sizes alone.
+// The fp32 values s and t enter an expansion as three bf16 terms (24 bits of
+// mantissa), so that y and dx are what fp32 products give up to their one
+// rounding, also where base takes the products away again. All reductions run
+// in an order that depends on the sizes alone.
 #include "adapters.h"
 #include "common.cuh"
 #include "lora_tc.h"
+#include "lora_terms.cuh"
 #include "lora_walk.cuh"
 #include "sm100.cuh"
 
@@ -41,15 +43,6 @@ E4B_DEV void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
 
 E4B_DEV float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-
-// (a, b) as bf16 pairs hi + lo; an infinite or NaN value has no second term.
-E4B_DEV void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  const float2 h = unpack2(hi);
-  const float la = fabsf(h.x) < INFINITY ? a - h.x : 0.f;
-  const float lb = fabsf(h.y) < INFINITY ? b - h.y : 0.f;
-  lo = pack_bf16x2(la, lb);
 }
 
 E4B_DEV uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
@@ -203,7 +196,7 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // strip), keeps its columns of W in registers while the group lasts, and takes a
 // tile's positions 16 at a time, the rows of base of the next kAhead sixteens
 // under way, past the end of the tile too (cp.async into the lane's own slots of
-// shared memory: no barrier). v's fragments (hi and lo terms, in the order of the MMA's
+// shared memory: no barrier). v's fragments (three terms, in the order of the MMA's
 // A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
 // strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
 // are eight consecutive columns: one 16-byte access to base, y and h. 8192 rows
@@ -231,7 +224,7 @@ struct Expand {
 
 constexpr int kAhead = 2;  // sixteens of base under way (one or three: 2 to 4 us more for 8192 rows of 28672)
 static_assert(kAhead == 2, "expand_kernel waits for at most two later ones");
-constexpr int kSixteens = kTile / 16;
+constexpr int kTerms = 3;
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
 
@@ -277,6 +270,9 @@ template <int KS, int GLU>
 constexpr int kStrips = KS > 2 && GLU == kGluNone ? 1 : 2;
 template <int KS, int GLU>
 constexpr int kExpandCtas = KS > 2 && kStrips<KS, GLU> == 2 ? 1 : 2;
+// Sixteens of a tile, at most: above rank 32 with two CTAs an SM the terms of four fit.
+template <int KS, int GLU>
+constexpr int kSixteens = KS > 2 && kExpandCtas<KS, GLU> == 2 ? 4 : kTile / 16;
 
 template <int KS, int GLU, int ACT, bool WT>
 __global__ void __launch_bounds__(kThreads, kExpandCtas<KS, GLU>)
@@ -286,7 +282,8 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
     int32_t g, cb, row0, n;
   };
   extern __shared__ uint4 smem[];
-  using Frags = uint4[kSixteens][KS][2][32];
+  constexpr int SIX = kSixteens<KS, GLU>, UNITS = SIX * KS * 32 / kThreads;  // places of the fragments a thread
+  using Frags = uint4[SIX][KS][kTerms][32];
   Frags* frags = reinterpret_cast<Frags*>(smem);                 // [2]
   uint4* ring = smem + 2 * sizeof(Frags) / sizeof(uint4);        // [kAhead + 1][2][ST][kThreads], with base
   __shared__ int32_t at[2][kTile];
@@ -357,15 +354,15 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
       }
     }
   };
-  // v's share of this thread: KS places of the tile's fragments, four values of
+  // v's share of this thread: its places of the tile's fragments, four values of
   // two rows each; and the row of position tid
-  float4 vr[KS][2];
+  float4 vr[UNITS][2];
   float vw = 1.f;
   int32_t vrow = -1;
   auto load_v = [&](const Item& t) {
     vw = e.scaled && d.scale ? __ldg(d.scale + t.g) : 1.f;
 #pragma unroll
-    for (int u = 0; u < KS; ++u) {
+    for (int u = 0; u < UNITS; ++u) {
       const int i = u * kThreads + tid, ks = (i >> 5) % KS, six = (i >> 5) / KS;
       const int m = 16 * six + (lane >> 2), j = 16 * ks + 4 * q;
 #pragma unroll
@@ -382,15 +379,17 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
   };
   auto store_v = [&](int buf) {
 #pragma unroll
-    for (int u = 0; u < KS; ++u) {
+    for (int u = 0; u < UNITS; ++u) {
       const int i = u * kThreads + tid, ks = (i >> 5) % KS, six = (i >> 5) / KS;
-      uint4 hi, lo;  // registers k and k + 2: row m + 8 k
-      split2(vw * vr[u][0].x, vw * vr[u][0].y, hi.x, lo.x);
-      split2(vw * vr[u][1].x, vw * vr[u][1].y, hi.y, lo.y);
-      split2(vw * vr[u][0].z, vw * vr[u][0].w, hi.z, lo.z);
-      split2(vw * vr[u][1].z, vw * vr[u][1].w, hi.w, lo.w);
-      frags[buf][six][ks][0][lane] = hi;
-      frags[buf][six][ks][1][lane] = lo;
+      uint32_t w[4][kTerms];  // registers k and k + 2: row m + 8 k
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        split_pair(vw * vr[u][k].x, vw * vr[u][k].y, w[k]);
+        split_pair(vw * vr[u][k].z, vw * vr[u][k].w, w[k + 2]);
+      }
+#pragma unroll
+      for (int part = 0; part < kTerms; ++part)
+        frags[buf][six][ks][part][lane] = make_uint4(w[0][part], w[1][part], w[2][part], w[3][part]);
     }
     if (tid < kTile) at[buf][tid] = vrow;
   };
@@ -490,7 +489,7 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part < kTerms; ++part) {
           const uint4 f = frags[buf][six][ks][part][lane];
 #pragma unroll
           for (int st = 0; st < ST; ++st)
@@ -618,12 +617,12 @@ cudaError_t launch_expand_of(const Adapters& d, Expand e, cudaStream_t st, int s
   // the largest tile (a sixteen's MMAs need its factors staged) of which there are
   // enough to go round: 128 rows of one group, r 64, 4096 columns took 19 us less so
   const int64_t ctas = int64_t(sms) * kExpandCtas<KS, GLU>, groups = d.G < d.R_max ? d.G : d.R_max;
-  e.tile.bits = 7;
+  e.tile.bits = kSixteens<KS, GLU> == 4 ? 6 : 7;
   while (e.tile.bits > 4 && e.col_blocks * ((d.R_max >> e.tile.bits) + (groups + 1) / 2) < ctas) --e.tile.bits;
   int64_t grid = e.col_blocks * pieces_bound(d.G, d.R_max, int64_t(1) << e.tile.bits);
   if (grid > ctas) grid = ctas;
   auto kernel = expand_kernel<KS, GLU, ACT, WT>;
-  constexpr int staged = 2 * kSixteens * KS * 64 * 16, ring = (kAhead + 1) * 2 * strips * kThreads * 16;
+  constexpr int staged = 2 * kSixteens<KS, GLU> * KS * kTerms * 32 * 16, ring = (kAhead + 1) * 2 * strips * kThreads * 16;
   const int smem = staged + (e.base ? ring : 0);
   static SmemAllowed allowed;
   const cudaError_t err = allow_smem(kernel, staged + ring, allowed);

@@ -52,6 +52,7 @@
 
 #include "common.cuh"
 #include "lora_tc.h"
+#include "lora_terms.cuh"
 #include "lora_walk.cuh"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -154,31 +155,14 @@ E4B_DEV bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit, const vol
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// (a, b) -= the bf16 pair h.
-E4B_DEV void less(float& a, float& b, uint32_t h) {
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "r"((h << 16) ^ 0x80000000u), "r"((h & 0xFFFF0000u) ^ 0x80000000u));
-}
-
-// Eight values as three bf16 terms; infinities and NaN have only the first.
+// Eight values as three bf16 terms.
 E4B_DEV void split3(float4 x, float4 y, float w, uint4 (&t)[3]) {
-  float v[8] = {w * x.x, w * x.y, w * x.z, w * x.w, w * y.x, w * y.y, w * y.z, w * y.w};
-  uint32_t q[3][4];
+  const float v[8] = {w * x.x, w * x.y, w * x.z, w * x.w, w * y.x, w * y.y, w * y.z, w * y.w};
+  uint32_t q[4][3];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float &a = v[2 * i], &b = v[2 * i + 1];
-    const uint32_t h = q[0][i] = pack_bf16x2(a, b);
-    less(a, b, h);
-    if ((h & 0x7F80u) == 0x7F80u) a = 0.f;
-    if ((h & 0x7F800000u) == 0x7F800000u) b = 0.f;
-    q[1][i] = pack_bf16x2(a, b);
-    less(a, b, q[1][i]);
-    q[2][i] = pack_bf16x2(a, b);
-  }
+  for (int i = 0; i < 4; ++i) split_pair(v[2 * i], v[2 * i + 1], q[i]);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) t[k] = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+  for (int k = 0; k < 3; ++k) t[k] = make_uint4(q[0][k], q[1][k], q[2][k], q[3][k]);
 }
 
 template <bool OUT, bool GRAD, int RP>  // RP: the rank's operand width, 16, 32 or 64

@@ -580,10 +580,9 @@ e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
  * rows of two positions must differ; an entry outside [0, rows) leaves its
  * position out (s[p] = 0, no row written, nothing added to the gradients).
  * Rows of no position are left as they were.
- * fp32 accumulation; s and t enter a product with a bf16 result as two bf16
- * terms (16 bits of mantissa), one with an fp32 result (da, db) as three (24
- * bits); every reduction runs in a fixed order, so repeated calls give the same
- * bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
+ * fp32 accumulation; s and t enter their products as three bf16 terms (24 bits
+ * of mantissa); every reduction runs in a fixed order, so repeated calls give
+ * the same bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
  * with zeros; an adapter of a higher rank is the sum of two, the second with
  * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max <= 2^30;
  * all pointers but offsets, row and scale 16-byte aligned. ws: device scratch of
