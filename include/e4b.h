@@ -581,7 +581,8 @@ e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
  * position out (s[p] = 0, no row written, nothing added to the gradients).
  * Rows of no position are left as they were.
  * fp32 accumulation; s and t enter their products as three bf16 terms (24 bits
- * of mantissa); every reduction runs in a fixed order, so repeated calls give
+ * of mantissa) of one sign, so that infinities become what they become in fp32
+ * (of factors above 2^-70 in magnitude); every reduction runs in a fixed order, so repeated calls give
  * the same bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
  * with zeros; an adapter of a higher rank is the sum of two, the second with
  * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max <= 2^30;

@@ -83,3 +83,73 @@ def test_row_gradients_keep_24_bits_of_t(r):
     e4b.e4b_lora_backward(a.cuda(), b.cuda(), None, None, dy, even_groups(c.G, c.each),
                           workspace(c.G, r, 8, c.C, c.R, True), dx=dx, dx_base=c.base.cuda())
     c.check(dx)
+
+
+# ------------------------------------------------------------- infinities
+def same_kind(got, want):
+    """Infinite, with the sign, and NaN at the same places."""
+    got, want = got.cpu().double(), want.cpu()
+    return torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.isinf(got), torch.isinf(want)) and \
+        torch.equal(got[torch.isinf(got)].sign(), want[torch.isinf(want)].sign())
+
+
+def infinite_case(r, seed=0):
+    """Factors of every kind: of 24 bits, of 8 (whose lower terms would be zero),
+    powers of two, of both signs."""
+    g = torch.Generator().manual_seed(seed + r)
+    G, each, K, N = 3, 37, 72, 80
+    R = G * each
+    a, b = torch.randn(G, r, K, generator=g).to(BF16), torch.randn(G, N, r, generator=g).to(BF16)
+    x, dy = torch.randn(R, K, generator=g).to(BF16), torch.randn(R, N, generator=g).to(BF16)
+    s = torch.randn(R, r, generator=g)
+    s[::3] = s[::3].to(BF16).float()
+    s[::5] = torch.sign(s[::5]) * 0.25
+    return G, each, K, N, R, a, b, x, dy, s, g
+
+
+@pytest.mark.parametrize("r", [8, 16, 40, 64])
+def test_infinite_rows_make_infinite_gradients(r):
+    G, each, K, N, R, a, b, x, dy, s, _ = infinite_case(r)
+    # t of 24 bits, of 8 and of one: of rows of dy with all, one and one simple value
+    dy[::3] = 0
+    dy[::3, 0] = 1.5
+    b[:, 0] = 0.5
+    t = torch.stack([dy[p].double() @ b[p // each].double() for p in range(R)])
+    x[5, 3], x[40, 9], x[42, 10], x[42, 11] = float("inf"), -float("inf"), float("inf"), -float("inf")
+    x[80, 20], x[81, 20] = float("inf"), float("inf")
+    da, db = torch.empty(G, r, K, device="cuda"), torch.empty(G, N, r, device="cuda")
+    off = even_groups(G, each)
+    ws = workspace(G, r, N, K, R, True)
+    e4b.e4b_lora_backward(a.cuda(), b.cuda(), x.cuda(), None, dy.cuda(), off, ws, da=da)
+    want = torch.stack([t[g * each:(g + 1) * each].T @ x[g * each:(g + 1) * each].double() for g in range(G)])
+    assert bool(torch.isinf(want).any()) and same_kind(da, want)
+    dy[6, 4], dy[41, 8], dy[45, 7] = float("inf"), -float("inf"), float("inf")
+    e4b.e4b_lora_backward(a.cuda(), b.cuda(), None, s.cuda(), dy.cuda(), off, ws, db=db)
+    want = torch.stack([dy[g * each:(g + 1) * each].double().T @ s[g * each:(g + 1) * each].double() for g in range(G)])
+    assert bool(torch.isinf(want).any()) and same_kind(db, want)
+
+
+@pytest.mark.parametrize("r", [8, 16, 40, 64])
+def test_infinite_weights_and_factors_make_infinite_rows(r):
+    G, each, K, N, R, a, b, x, dy, s, _ = infinite_case(r, 1)
+    off = even_groups(G, each)
+    x[::4] = 0
+    x[::4, 0] = 2.0  # s of few bits
+    a[:, :, 0] = a[:, :, 0].sign() * 0.5
+    b[1, 7, 2], b[1, 20, r - 1], b[2, 9, 0] = float("inf"), -float("inf"), float("inf")
+    x[30, 5] = float("inf")  # an infinite factor
+    y = torch.empty(R, N, dtype=BF16, device="cuda")
+    e4b.e4b_lora(a.cuda(), b.cuda(), x.cuda(), off, workspace(G, r, N, K, R, False), y=y)
+    xa = torch.stack([a[p // each].double() @ x[p].double() for p in range(R)])
+    want = torch.stack([b[p // each].double() @ xa[p] for p in range(R)])
+    assert bool(torch.isinf(want).any()) and same_kind(y, want)
+    b[~torch.isfinite(b.float())] = 1.0
+    dy[::4] = 0
+    dy[::4, 0] = 2.0
+    b[:, 0] = 0.25
+    a[0, 3, 7], a[1, 0, 9], a[2, r - 1, 11] = float("inf"), -float("inf"), float("inf")
+    dx = torch.empty(R, K, dtype=BF16, device="cuda")
+    e4b.e4b_lora_backward(a.cuda(), b.cuda(), None, None, dy.cuda(), off, workspace(G, r, N, K, R, True), dx=dx)
+    t = torch.stack([dy[p].double() @ b[p // each].double() for p in range(R)])
+    want = torch.stack([t[p] @ a[p // each].double() for p in range(R)])
+    assert bool(torch.isinf(want).any()) and same_kind(dx, want)
