@@ -31,15 +31,6 @@ E4B_DEV uint4 pack8(const float (&a)[8]) {
                     pack_bf16x2(a[6], a[7]));
 }
 
-// The hardware exp2 and reciprocal (relative error ~2^-20, far below bf16's
-// half step). Below -87 the reciprocal flushes to zero, where the exact value
-// is under 2^-125.
-E4B_DEV float fast_sigmoid(float v) {
-  float s;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + __expf(-v)));
-  return s;
-}
-
 struct GluRows {
   const uint16_t* gu;
   int64_t ld_gu;
@@ -98,7 +89,7 @@ struct GluVec {
     }
     if constexpr (!BACKWARD) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) h[i] = glu_act(CLAMPED ? E4B_ACT_CLAMPED_GLU : E4B_ACT_SWIGLU, g[i], u[i], r.alpha, r.limit);
+      for (int i = 0; i < P; ++i) h[i] = gated<CLAMPED>(g[i], u[i], r.alpha, r.limit);
     } else {
       float dw[8], dg[P], du[P];
       unpack8(d, dw);
@@ -110,9 +101,9 @@ struct GluVec {
         const bool uout = CLAMPED && (u[i] > r.limit || u[i] < -r.limit);
         const float gc = gout ? r.limit : g[i];
         const float uc = CLAMPED ? (uout ? copysignf(r.limit, u[i]) : u[i]) + 1.f : u[i];
-        const float sg = fast_sigmoid(slope * gc);
+        const float sg = gate_sigmoid(gc, slope);
         const float f = gc * sg;
-        h[i] = f * uc;
+        h[i] = f * uc;  // as gated() has it
         // sg (1 + a g' (1 - sg)) as sg + a (g' sg) (1 - sg): no factor overflows where the gate is closed
         dg[i] = gout ? 0.f : dw[i] * (uc * fmaf(slope * f, 1.f - sg, sg));
         du[i] = uout ? 0.f : dw[i] * f;

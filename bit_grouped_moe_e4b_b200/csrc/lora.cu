@@ -228,24 +228,6 @@ constexpr int kTerms = 3;
 
 enum { kGluNone = 0, kGluHalves = 1, kGluInterleaved = 2 };
 
-// The activation of an expanded pair: exp2 and the reciprocal without their
-// handling of denormals, six instructions a value for SwiGLU instead of 16. Where
-// the reciprocal flushes to zero the exact factor is under 2^-125. The gate meets
-// its sigmoid before the up value, so that no product overflows on the way to a
-// finite result.
-template <int ACT>
-E4B_DEV float activate(float g, float u, float alpha, float limit) {
-  if constexpr (ACT == E4B_ACT_CLAMPED_GLU) {
-    g = g > limit ? limit : g;
-    u = (u > limit ? limit : (u < -limit ? -limit : u)) + 1.f;
-  }
-  const float slope = ACT == E4B_ACT_CLAMPED_GLU ? alpha : 1.f;
-  float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (slope * -1.4426950408889634f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-  return (g * s) * u;
-}
-
 E4B_DEV uint4 pack8(const float (&a)[8]) {
   return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
                     pack_bf16x2(a[6], a[7]));
@@ -512,14 +494,14 @@ expand_kernel(const __grid_constant__ Adapters d, const __grid_constant__ Expand
         if constexpr (GLU == kGluHalves) {
           float h[8];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) h[p] = activate<ACT>(v[0][p], v[1][p], e.alpha, e.limit);
+          for (int p = 0; p < 8; ++p) h[p] = gated<ACT == E4B_ACT_CLAMPED_GLU>(v[0][p], v[1][p], e.alpha, e.limit);
           if (cols.in[0]) *reinterpret_cast<uint4*>(e.h + place(row[i], e.ld_h) + cols.c[0]) = pack8(h);
         } else if constexpr (GLU == kGluInterleaved) {
 #pragma unroll
           for (int st = 0; st < ST; ++st) {
             float h[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) h[p] = activate<ACT>(v[st][2 * p], v[st][2 * p + 1], e.alpha, e.limit);
+            for (int p = 0; p < 4; ++p) h[p] = gated<ACT == E4B_ACT_CLAMPED_GLU>(v[st][2 * p], v[st][2 * p + 1], e.alpha, e.limit);
             if (cols.in[st])
               *reinterpret_cast<uint2*>(e.h + place(row[i], e.ld_h) + cols.c[st] / 2) =
                   make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
