@@ -579,16 +579,33 @@ ContractArgs contract_of(const e4b_lora_args& a, const uint16_t* z, int64_t ld_z
 // 12.2 and 11.8 against 8.7 and 9.1, rank 64 21.3 and 19.7 against 18.9 and 21.5.
 bool forward_uses_tiles(int64_t R_max, int64_t K, int r) { return double(R_max) * double(K) * r > 2e8; }
 
-// Parts of s. Few rows: enough CTAs to fill the GPU, each with at least one
-// 32-wide chunk a warp.
+// Parts of s that warps make, at most: one 32-wide chunk a warp, 16.
+int64_t most_slices(int64_t K) {
+  const int64_t most = (K + 32 * kWarps - 1) / (32 * kWarps);
+  return most < 16 ? most : 16;
+}
+
+// Parts of s. Few rows: enough CTAs to fill the GPU.
 int forward_slices(int G, int r, int64_t K, int64_t R_max, int sms) {
   if (forward_uses_tiles(R_max, K, r)) return contract_blocks(G, r, K, R_max, true, false, sms);
   const int64_t tiles = pieces_bound(G, R_max, kShrinkRows);
-  const int64_t most = (K + 32 * kWarps - 1) / (32 * kWarps);
   int64_t want = sms / (tiles > 0 ? tiles : 1);
-  if (want > 16) want = 16;
-  if (want > most) want = most;
+  if (want > most_slices(K)) want = most_slices(K);
   return int(want < 1 ? 1 : want);
+}
+
+// At least forward_slices() times the rows, for every number of rows up to R_max.
+// By warps, beyond one slice: 32 rows a CTA or fewer (there are R / 32 + min(G, R)
+// pieces or none) and no more CTAs than SMs.
+int64_t forward_part_rows(int G, int r, int64_t K, int64_t R_max, int sms) {
+  int64_t found = R_max;
+  const int64_t sliced = most_slices(K) * R_max, cap = int64_t(kShrinkRows) * sms;
+  if (found < sliced && found < cap) found = sliced < cap ? sliced : cap;
+  if (forward_uses_tiles(R_max, K, r)) {
+    const int64_t rows = contract_out_rows(G, r, K, R_max, false, sms);
+    if (found < rows) found = rows;
+  }
+  return found;
 }
 
 template <int KS, int GLU, int ACT, bool WT>
@@ -635,23 +652,20 @@ cudaError_t launch_shrink(const Adapters& d, const e4b_lora_args& a, int slices,
   return launch_dependent(shrink_kernel<JT>, dim3(tiles, slices), dim3(kThreads), 0, st, d, a.x, a.ld_x, slices, s);
 }
 
+// Sections that are large enough for every number of rows up to R_max.
 struct BackPlan {
-  int parts;  // of t
   size_t t_part, t, db_part, da_part, total;
 };
 
 BackPlan plan_backward(int G, int r, int64_t N, int64_t K, int64_t R_max, int sms) {
   BackPlan p;
   // t alone is cut otherwise than t and db together: room for either
-  const int a = contract_blocks(G, r, N, R_max, true, true, sms), b = contract_blocks(G, r, N, R_max, true, false, sms);
-  p.parts = a > b ? a : b;
+  const int64_t a = contract_out_rows(G, r, N, R_max, true, sms), b = contract_out_rows(G, r, N, R_max, false, sms);
   size_t o = 0;
-  p.t_part = o;  o = align256(o + size_t(p.parts) * R_max * r * 4);
+  p.t_part = o;  o = align256(o + size_t(a > b ? a : b) * r * 4);
   p.t = o;       o = align256(o + size_t(R_max) * r * 4);
-  p.db_part = o;
-  const size_t n = contract_part_bytes(G, r, N, R_max, true, sms), n1 = contract_part_bytes(G, r, N, R_max, false, sms);
-  o = align256(o + (n > n1 ? n : n1));
-  p.da_part = o; o = align256(o + contract_part_bytes(G, r, K, R_max, false, sms));
+  p.db_part = o; o = align256(o + contract_part_bytes(r, N, false, sms));  // with t there are no more
+  p.da_part = o; o = align256(o + contract_part_bytes(r, K, false, sms));
   p.total = o;
   return p;
 }
@@ -660,7 +674,7 @@ BackPlan plan_backward(int G, int r, int64_t N, int64_t K, int64_t R_max, int sm
 
 size_t lora_workspace_bytes(int64_t G, int r, int64_t N, int64_t K, int64_t R_max, bool back, int sms) {
   if (back) return plan_backward(int(G), r, N, K, R_max, sms).total + 256;
-  return align256(size_t(forward_slices(int(G), r, K, R_max, sms)) * size_t(R_max) * r * 4) + 256;
+  return align256(size_t(forward_part_rows(int(G), r, K, R_max, sms)) * r * 4) + 256;
 }
 
 cudaError_t launch_lora(const e4b_lora_args& a, void* ws, uint32_t flags, cudaStream_t st, int sms, int* launches) {

@@ -786,36 +786,56 @@ struct Plan {
   int rp, chunks, blocks, vbufs, stages;
 };
 
-// Column tiles of a block: at most those whose gradients TMEM holds, and of
-// these the number with the least time by this estimate, in units of one tile's
-// 32 KB from HBM: the longest run's items (for each, besides its tiles, half a
-// unit, or with a gradient of a wide rank, whose terms have one buffer, more),
-// the last gradients' way out of TMEM, the parts of `out` written and read
-// again. Row tiles are an estimate: groups may end anywhere in one.
+int operand_width(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+
+// The choices of a pass' column tiles a block: at most those whose gradients TMEM
+// holds; without a gradient up to 64, in steps that grow (this runs on the host
+// for every call).
+struct Choices {
+  int r, sms, most;
+  int64_t all;  // column tiles
+  bool out, grad;
+  Choices(int rank, int64_t C, bool o, bool g, int n) : r(rank), sms(n), all((C + kTile - 1) / kTile), out(o), grad(g) {
+    const int rp = operand_width(rank);
+    most = g ? (512 - (o ? 2 * rp : 0)) / grad_width(rp) : 64;
+    if (g && most > kMaxChunks) most = kMaxChunks;
+    if (most > all) most = int(all);
+  }
+  int after(int c) const { return c + (grad || c < 4 ? 1 : c < 16 ? 4 : 16); }
+  int64_t blocks(int c) const { return (all + c - 1) / c; }
+  // The estimated time, in units of one tile's 32 KB from HBM: the longest run's
+  // items (for each, besides its tiles, half a unit, or with a gradient of a wide
+  // rank, whose terms have one buffer, more), the last gradients' way out of TMEM,
+  // the parts of `out` written and read again.
+  double item(int c) const { return double(c) + (grad && operand_width(r) == 64 ? 1.5 : 0.5); }
+  double last(int c) const { return grad ? 0.5 * double(c) : 0.0; }
+  double parts(int c) const { return out && blocks(c) > 1 ? double(blocks(c)) * r / (32.0 * sms) : 0.0; }
+  double time(int c, int64_t tiles) const {
+    return double((blocks(c) * tiles + sms - 1) / sms) * item(c) + last(c) + parts(c) * double(tiles);
+  }
+};
+
+// Row tiles, an estimate: groups may end anywhere in one. Never fewer for more rows.
+int64_t row_tiles(int G, int64_t R_max) {
+  const int64_t groups = G < R_max ? G : R_max, tiles = R_max / kTile + (groups + 1) / 2;
+  return tiles < groups ? groups : tiles;
+}
+
 Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms) {
   Plan q;
-  q.rp = r <= 16 ? 16 : r <= 32 ? 32 : 64;
-  const int gw = grad_width(q.rp);
-  int most = grad ? (512 - (out ? 2 * q.rp : 0)) / gw : 64;
-  if (grad && most > kMaxChunks) most = kMaxChunks;
-  const int64_t all = (C + kTile - 1) / kTile;
-  const int64_t groups = G < R_max ? G : R_max;
-  int64_t tiles = R_max / kTile + (groups + 1) / 2;  // > 0, if there are rows
-  if (tiles < groups) tiles = groups;
+  q.rp = operand_width(r);
+  const Choices ch(r, C, out, grad, sms);
+  const int64_t tiles = row_tiles(G, R_max);
   double best = 0;
   q.chunks = 0;
-  // without a gradient up to 64 tiles, in steps that grow: this runs on the host for every call
-  for (int64_t c = 1; c <= most && c <= all; c += grad || c < 4 ? 1 : c < 16 ? 4 : 16) {
-    const int64_t blocks = (all + c - 1) / c, items = blocks * tiles;
-    double t = double((items + sms - 1) / sms) * (double(c) + (grad && q.rp == 64 ? 1.5 : 0.5));
-    if (grad) t += 0.5 * double(c);
-    if (out && blocks > 1) t += double(items) * r / (32.0 * sms);
+  for (int c = 1; c <= ch.most; c = ch.after(c)) {
+    const double t = ch.time(c, tiles);
     if (!q.chunks || t <= best) {
       best = t;
-      q.chunks = int(c);
+      q.chunks = c;
     }
   }
-  q.blocks = int((all + q.chunks - 1) / q.chunks);
+  q.blocks = int(ch.blocks(q.chunks));
   q.vbufs = q.rp <= 32 ? 2 : 1;
   const int64_t terms = grad ? int64_t(q.vbufs) * 6 * kTile * q.rp : 0;
   const int64_t stage = kZBytes + (out ? 2 * kTile * q.rp : 0);
@@ -824,7 +844,7 @@ Plan plan_of(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sm
   return q;
 }
 
-int64_t part_floats(int r, const Plan& q, int sms) { return int64_t(2) * sms * q.chunks * kTile * r; }
+int64_t part_floats(int r, int chunks, int sms) { return int64_t(2) * sms * chunks * kTile * r; }
 
 Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   Pass p{};
@@ -840,7 +860,7 @@ Pass pass_of(const ContractArgs& a, const Plan& q, int sms) {
   p.v = a.v;
   p.grad = a.grad;
   p.grad_part = a.grad_part;
-  p.notes = a.grad ? reinterpret_cast<Note*>(a.grad_part + part_floats(a.r, q, sms)) : nullptr;
+  p.notes = a.grad ? reinterpret_cast<Note*>(a.grad_part + part_floats(a.r, q.chunks, sms)) : nullptr;
   p.status = a.status;
   p.G = a.G;
   p.r = a.r;
@@ -882,8 +902,40 @@ int contract_blocks(int G, int r, int64_t C, int64_t R_max, bool out, bool grad,
   return plan_of(G, r, C, R_max, out, grad, sms).blocks;
 }
 
-size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int sms) {
-  return size_t(part_floats(r, plan_of(G, r, C, R_max, out, true, sms), sms)) * 4 + size_t(2) * sms * sizeof(Note);
+// A pass takes c column tiles a block only where no other choice d is estimated
+// to be faster. With time(c) >= rate(c) tiles + last(c), rate the time a row tile,
+// and time(d) < rate(d) tiles + item(d) + last(d) this ends at
+//   tiles = (item(d) + last(d) - last(c)) / (rate(c) - rate(d)), rate(c) > rate(d),
+// whatever the longest runs are rounded to. So c's parts are no more than those of
+// the most rows with as few tiles.
+int64_t contract_out_rows(int G, int r, int64_t C, int64_t R_max, bool grad, int sms) {
+  const Choices ch(r, C, true, grad, sms);
+  const int64_t tiles = row_tiles(G, R_max);
+  auto rate = [&](int c) { return double(ch.blocks(c)) * ch.item(c) / sms + ch.parts(c); };
+  int64_t found = R_max;
+  for (int c = 1; c <= ch.most; c = ch.after(c)) {
+    double end = double(tiles);
+    for (int d = 1; d <= ch.most; d = ch.after(d)) {
+      const double more = rate(c) - rate(d);
+      if (more > 1e-9) {
+        const double e = (ch.item(d) + ch.last(d) - ch.last(c)) / more + 1.0;  // 1: for the roundings here
+        if (e < end) end = e;
+      }
+    }
+    if (end < 1.0) continue;
+    const int64_t t = int64_t(end);
+    // the most rows of at most t tiles: below G rows each is one
+    int64_t rows = R_max;
+    if (t < tiles) rows = t < G ? t : kTile * (t - (G + 1) / 2) + kTile - 1;
+    if (rows < G && t >= G) rows = G;
+    if (rows > R_max) rows = R_max;
+    if (ch.blocks(c) * rows > found) found = ch.blocks(c) * rows;
+  }
+  return found;
+}
+
+size_t contract_part_bytes(int r, int64_t C, bool out, int sms) {
+  return size_t(part_floats(r, Choices(r, C, out, true, sms).most, sms)) * 4 + size_t(2) * sms * sizeof(Note);
 }
 
 cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms) {

@@ -41,8 +41,11 @@ struct ContractArgs {
 
 // Column blocks of a pass: parts of `out`.
 int contract_blocks(int G, int r, int64_t C, int64_t R_max, bool out, bool grad, int sms);
-// Bytes of grad_part.
-size_t contract_part_bytes(int G, int r, int64_t C, int64_t R_max, bool out, int sms);
+// At least the column blocks of a pass with `out` times its rows, for every
+// number of rows up to R_max; never less for more rows.
+int64_t contract_out_rows(int G, int r, int64_t C, int64_t R_max, bool grad, int sms);
+// Bytes of grad_part, whatever the rows.
+size_t contract_part_bytes(int r, int64_t C, bool out, int sms);
 cudaError_t launch_contract(const ContractArgs& a, cudaStream_t st, int sms);
 // What a pass with `grad` leaves to do: the sums of groups whose rows several
 // CTAs took, zeros for groups without rows. After launch_contract, with the

@@ -627,7 +627,9 @@ typedef struct {
   int32_t* status; /* optional device int32 that records E4B_ERR_DEVICE_TIMEOUT */
 } e4b_lora_args;
 
-/* Host: workspace bytes of e4b_lora (backward == 0) or e4b_lora_backward. */
+/* Host: workspace bytes of e4b_lora (backward == 0) or e4b_lora_backward with
+ * at most R_max positions: never fewer bytes for more, so a workspace for the
+ * largest batch serves the smaller ones (same G, r, N, K). */
 e4b_status e4b_lora_workspace_size(int32_t G, int32_t r, int64_t N, int64_t K, int64_t R_max, int32_t backward,
                                    size_t* bytes);
 e4b_status e4b_lora(const e4b_lora_args* args, void* ws, size_t ws_bytes, uint32_t flags, void* stream);
