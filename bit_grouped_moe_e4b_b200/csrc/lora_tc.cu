@@ -306,9 +306,10 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
     }
   };
 
-  // the MMAs that this thread issued have to finish before TMEM is freed
+  // The MMAs that this thread issued, and their arrivals, have to finish before TMEM
+  // is freed and the CTA ends. No other role's end says so: one that gives up after
+  // this thread's last issue does not wait for it.
   auto drain = [&](uint64_t* bar) {
-    if (!*s_abort) return;  // the results' warps have waited for them
     mma_commit(bar);
     mbar_wait_bounded(bar, 0, kWaitPolls, nullptr);
   };

@@ -1,4 +1,5 @@
-"""The adapter path's calls at their edges: workspaces of other batches."""
+"""The adapter path's calls at their edges: workspaces of other batches, waits
+that give up in every kind of pass."""
 
 import pytest
 import torch
@@ -33,3 +34,31 @@ def test_one_workspace_for_smaller_batches(counts, r, K, N):
         for whole, n in held:
             assert bool((whole[n:] == 255).all())
     assert int(c.status) == 0
+
+
+FORMS = [("da", "db", "dx"), ("da",), ("db",), ("dx",)]  # passes of both kinds, of gradients alone, of rows alone
+
+
+def only(c, s, form, **kw):
+    """c's backward with the results that `form` names."""
+    return c.backward(s, **{k: None for k in ("dx", "da", "db") if k not in form}, **kw)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+@pytest.mark.parametrize("mapped", [False, True])
+@pytest.mark.parametrize("r", [16, 64])
+def test_waits_that_give_up_anywhere_leave_the_next_call_right(r, mapped, form):
+    # which role gives up first is a matter of timing: each must drain its own work
+    c = Case([900, 130, 0, 2300], r, 1096, 1544, mapped=mapped, seed=22)
+    s = c.s()
+    want = only(c, s, form)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        only(c, s, form, flags=e4b.FLAG_TEST_TIMEOUT)
+        assert e4b.e4b_status_string(int(c.status)) == "device wait timed out"
+        c.status.zero_()
+        got = only(c, s, form)
+        assert int(c.status) == 0
+        for k in form:
+            same = (lambda t: t[c.used]) if k == "dx" else (lambda t: t)
+            assert torch.equal(same(got[k]), same(want[k])), k
