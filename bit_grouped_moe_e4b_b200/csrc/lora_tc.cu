@@ -316,7 +316,9 @@ contract_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_consta
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
-    if (lane == 0) {
+    // Mapped rows of a gradient alone need no copy, and nobody waits for `full`:
+    // walking their stages this thread could fall a whole ring behind.
+    if (lane == 0 && (OUT || !p.row)) {
       Ring st(p.stages);
       int64_t i = 0;
       bool aborted = false;

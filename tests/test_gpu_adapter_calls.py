@@ -62,3 +62,17 @@ def test_waits_that_give_up_anywhere_leave_the_next_call_right(r, mapped, form):
         for k in form:
             same = (lambda t: t[c.used]) if k == "dx" else (lambda t: t)
             assert torch.equal(same(got[k]), same(want[k])), k
+
+
+@pytest.mark.parametrize("form", [("da",), ("db",), ("da", "db")], ids=str)
+def test_mapped_gradients_alone_over_many_stages(form):
+    # nothing comes by TMA in these passes; stages go round many times
+    c = Case([9000, 0, 3000], 16, 1544, 1288, mapped=True, seed=23)
+    s = c.s()
+    want = c.backward(s)
+    c.check_backward(s, want)
+    for _ in range(5):
+        got = only(c, s, form)
+        for k in form:
+            assert float((got[k] - want[k]).norm()) <= 2 ** -20 * float(want[k].norm()), k  # cut otherwise, in fp32
+    assert int(c.status) == 0
