@@ -57,14 +57,20 @@ class Kept:
 
 @dataclass
 class Buffers:
-    """Named device buffers, allocated at their first use and kept: results and
-    kept rows of one step overwrite those of the step before."""
+    """Named device buffers, allocated at their first use and kept for as long as
+    this object lives, so that a CUDA graph may hold their addresses: one of each
+    name, shape, type and device. Results and kept rows of a step overwrite those of
+    the step before it of the same shapes; one Buffers serves one step at a time, on
+    one stream (two streams, or a graph beside an eager step, take two). Every batch
+    size that comes up keeps its own buffers: a program whose sizes vary without end
+    calls without, and lets the allocator serve it."""
     held: dict = field(default_factory=dict)
 
     def __call__(self, name, shape, dtype, device):
-        t = self.held.get(name)
-        if t is None or t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device:
-            t = self.held[name] = torch.empty(shape, dtype=dtype, device=device)
+        key = (name, tuple(shape), dtype, torch.device(device))
+        t = self.held.get(key)
+        if t is None:
+            t = self.held[key] = torch.empty(shape, dtype=dtype, device=device)
         return t
 
 

@@ -1,0 +1,42 @@
+"""The adapter layer as programs call it beside the plain step: other batch sizes
+between a graph's replays."""
+
+import pytest
+import torch
+
+from bit_grouped_moe_e4b_b200 import qlora
+from test_gpu_qlora import CASES, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def tensors(y, back):
+    dx, dgates, gu, dn = back
+    return [y, dx, dgates, gu.a, gu.b, dn.a, dn.b]
+
+
+def test_another_batch_size_between_replays():
+    c = Case(*CASES[1])
+    buf = qlora.Buffers()
+    x, ids, gates, dy = c.x.cuda(), c.ids.cuda(), c.gates.cuda(), c.dy.cuda()
+
+    def step(n):
+        y, kept = qlora.forward(c.layer, *c.dev, x[:n], ids[:n], gates[:n], buf)
+        return tensors(y, qlora.backward(c.layer, *c.dev, kept, dy[:n], buffers=buf))
+    T = x.shape[0]
+    step(T)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(T)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    small = [t.clone() for t in step(T // 3)]
+    # memory that was free after the smaller step
+    held = [torch.full((1 << 18,), 7.0, device="cuda") for _ in range(40)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(bool((h == 7.0).all()) for h in held)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(torch.equal(a, b) for a, b in zip(step(T // 3), small))
