@@ -507,6 +507,7 @@ e4b_status e4b_unpermute_backward(const uint16_t* dy, int64_t ld_dy, const uint1
   if (st != E4B_OK) return st;
   g_last_launches = 0;
   if (T == 0) return E4B_OK;
+  if (R_max == 0 && !dgates) return E4B_OK;  // dys has no rows, and perhaps no address
   if (!inv_perm || (!dys && !dgates)) return E4B_ERR_INVALID_ARG;
   if ((st = check_rows(dy, ld_dy, H)) != E4B_OK) return st;
   if (R_max > 0 && dgates && (st = check_rows(ys, ld_ys, H)) != E4B_OK) return st;
@@ -596,6 +597,7 @@ e4b_status e4b_lora_backward(const e4b_lora_args* a, void* ws, size_t ws_bytes, 
   e4b_status st = check_lora_sizes(a->G, a->r, a->N, a->K, a->R_max);
   if (st != E4B_OK) return st;
   g_last_launches = 0;
+  if (a->R_max == 0 && !a->da && !a->db) return E4B_OK;  // dx has no rows, and perhaps no address
   if (!a->dx && !a->da && !a->db) return E4B_ERR_INVALID_ARG;
   if ((st = check_lora(a, ws, ws_bytes, true)) != E4B_OK) return st;
   if (a->R_max > 0) {  // without rows the gradients are still set

@@ -489,8 +489,8 @@ e4b_status e4b_ep_combine(const uint16_t* ys, int64_t H, const int32_t* inv_perm
  * with a stride (ld_*, in values) of at least H that is a multiple of 8. A
  * slot or position outside the given sizes is treated as dropped. Sums run in
  * fp32 in slot order and are rounded once, so repeated calls give the same
- * bits. T == 0 or R_max == 0 is a no-op. T * top_k < 2^31. No output may
- * overlap an input.
+ * bits. T == 0 is a no-op; with R_max == 0 every slot counts as dropped (y, dx
+ * and dgates are 0). T * top_k < 2^31. No output may overlap an input.
  */
 
 /* xs[p] = x[perm[p] / top_k] for p < min(offsets[E], R_max); the other rows of

@@ -1,5 +1,5 @@
 """The adapter path's calls at their edges: workspaces of other batches, waits
-that give up in every kind of pass."""
+that give up in every kind of pass, no rows at all."""
 
 import pytest
 import torch
@@ -76,3 +76,41 @@ def test_mapped_gradients_alone_over_many_stages(form):
         for k in form:
             assert float((got[k] - want[k]).norm()) <= 2 ** -20 * float(want[k].norm()), k  # cut otherwise, in fp32
     assert int(c.status) == 0
+
+
+def test_without_rows_tokens_and_gates_get_zeros():
+    T, k, H = 5, 3, 72
+    BF16, F32 = torch.bfloat16, torch.float32
+    inv = torch.arange(T * k, dtype=torch.int32, device="cuda")  # every position is behind the last row
+    gates = torch.full((T, k), float("nan"), device="cuda")      # of dropped slots: not read
+    rows = torch.empty(0, H, dtype=BF16, device="cuda")
+    for g in (gates, None):
+        y = torch.full((T, H), 3.0, dtype=BF16, device="cuda")
+        e4b.e4b_unpermute(rows, inv, g, y, top_k=k)
+        assert not bool(y.any())
+    dx = torch.full((T, H), 3.0, dtype=BF16, device="cuda")
+    e4b.e4b_permute_backward(rows, inv, dx, top_k=k)
+    assert not bool(dx.any())
+    dy, dgates = torch.ones(T, H, dtype=BF16, device="cuda"), torch.full((T, k), 3.0, device="cuda")
+    e4b.e4b_unpermute_backward(dy, rows, inv, gates, torch.empty_like(rows), dgates, top_k=k)
+    assert not bool(dgates.any())
+    e4b.e4b_unpermute_backward(dy, rows, inv, gates, torch.empty_like(rows), None, top_k=k)
+    e4b.e4b_permute(torch.ones(T, H, dtype=BF16, device="cuda"), inv, torch.zeros(3, dtype=torch.int64, device="cuda"),
+                    torch.empty_like(rows), top_k=k)
+
+
+def test_adapters_without_rows():
+    G, r, K, N = 3, 16, 64, 96
+    BF16 = torch.bfloat16
+    a, b = torch.ones(G, r, K, dtype=BF16, device="cuda"), torch.ones(G, N, r, dtype=BF16, device="cuda")
+    off = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
+    x, y = torch.empty(0, K, dtype=BF16, device="cuda"), torch.empty(0, N, dtype=BF16, device="cuda")
+    s = torch.empty(0, r, device="cuda")
+    ws = torch.empty(e4b.e4b_lora_workspace_size(G, r, N, K, 0, True), dtype=torch.uint8, device="cuda")
+    e4b.e4b_lora(a, b, x, off, ws, base=y, y=y, s=s)
+    e4b.e4b_lora_backward(a, b, None, None, y, off, ws, dx=x, dx_base=x)
+    da, db = torch.full((G, r, K), 3.0, device="cuda"), torch.full((G, N, r), 3.0, device="cuda")
+    e4b.e4b_lora_backward(a, b, x, s, y, off, ws, dx=x, dx_base=x, da=da, db=db, accumulate=True)
+    assert bool((da == 3.0).all()) and bool((db == 3.0).all())
+    e4b.e4b_lora_backward(a, b, x, s, y, off, ws, dx=x, dx_base=x, da=da, db=db)
+    assert not bool(da.any()) and not bool(db.any())
