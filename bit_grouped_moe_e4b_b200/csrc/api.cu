@@ -542,10 +542,8 @@ static e4b_status check_lora_sizes(int32_t G, int32_t r, int64_t N, int64_t K, i
   if (G <= 0 || r <= 0 || N <= 0 || K <= 0 || R_max < 0) return E4B_ERR_INVALID_ARG;
   if (r % 8 || r > kLoraMaxRank || N % 8 || K % 8 || G > 1024) return E4B_ERR_UNSUPPORTED;
   if (R_max > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return E4B_ERR_UNSUPPORTED;
-  // (column block, row tile) pairs are counted in 31 bits: at most one per 32
-  // rows and 256 columns, plus one per group and 256 columns
-  const int64_t cols = (N > K ? N : K) / 256 + 1;
-  if ((R_max / 32 + G + 1) > (int64_t(1) << 31) / cols) return E4B_ERR_UNSUPPORTED;
+  // more values than any memory holds: parts and their places stay far below 63 bits
+  if (R_max > (int64_t(1) << 44) / (N > K ? N : K)) return E4B_ERR_UNSUPPORTED;
   return E4B_OK;
 }
 

@@ -585,7 +585,8 @@ e4b_status e4b_glu_backward(const e4b_glu_args* args, void* stream);
  * (of factors above 2^-70 in magnitude); every reduction runs in a fixed order, so repeated calls give
  * the same bits. Limits: r a multiple of 8, at most 64 (pad smaller ranks
  * with zeros; an adapter of a higher rank is the sum of two, the second with
- * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max <= 2^30;
+ * the first one's y as base); N % 8 == 0, K % 8 == 0; G <= 1024; R_max,
+ * N and K <= 2^30, R_max * N and R_max * K <= 2^44;
  * all pointers but offsets, row and scale 16-byte aligned. ws: device scratch of
  * e4b_lora_workspace_size bytes (16-byte aligned), for one call at a time.
  * flags: E4B_FLAG_ACCUMULATE (backward), E4B_FLAG_TEST_TIMEOUT. A wait on the GPU

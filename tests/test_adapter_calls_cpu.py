@@ -3,7 +3,7 @@
 import ctypes
 
 from bit_grouped_moe_e4b_b200 import e4b
-from test_adapters_cpu import INVALID, OK, P, lora_args
+from test_adapters_cpu import INVALID, OK, P, UNSUPPORTED, lora_args
 
 
 def test_results_without_rows_need_no_address():
@@ -19,3 +19,18 @@ def test_results_without_rows_need_no_address():
     for R, status in ((0, OK), (8, INVALID)):
         a = lora_args(R_max=R, **empty)
         assert L.e4b_lora_backward(ctypes.byref(a), P, n, 0, None) == status
+
+
+def test_sizes_up_to_the_limits_are_accepted():
+    def size(G, r, N, K, R):
+        return [e4b.e4b_lora_workspace_size(G, r, N, K, R, backward) for backward in (False, True)]
+
+    for G, r, N, K, R in ((1024, 64, 1 << 30, 64, 1 << 14), (1024, 8, 64, 1 << 30, 1 << 14), (1, 8, 1 << 14, 1 << 14, 1 << 30),
+                          (1024, 64, 1 << 14, 8, 1 << 30)):
+        s, t = size(G, r, N, K, R)
+        assert s >= R * r * 4 and t >= 2 * R * r * 4
+    for G, r, N, K, R in ((4, 16, 1 << 30, 64, (1 << 14) + 1), (4, 16, 64, (1 << 14) + 8, 1 << 30), (4, 16, (1 << 30) + 8, 64, 8),
+                          (4, 16, 64, 64, (1 << 30) + 1)):
+        for backward in (0, 1):
+            n = ctypes.c_size_t(0)
+            assert e4b.lib().e4b_lora_workspace_size(G, r, N, K, R, backward, ctypes.byref(n)) == UNSUPPORTED
