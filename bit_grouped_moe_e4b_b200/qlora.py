@@ -11,8 +11,9 @@ The packed weights are never unpacked to memory: both projections and their
 input gradients run on the packed bytes (e4b_grouped_gemm, e4b_grouped_dgrad),
 the steps between them are e4b_permute / e4b_unpermute, e4b_lora and e4b_glu.
 gu is kept in bf16, since the backward pass needs it. All work is enqueued on
-the current stream; no call synchronises, so forward and backward can be
-captured into a CUDA graph with buffers that the caller keeps (``Buffers``).
+the current stream of x's (dy's) device; no call synchronises, so forward and
+backward can be captured into a CUDA graph with buffers that the caller keeps
+(``Buffers``).
 """
 
 from __future__ import annotations
@@ -98,7 +99,11 @@ def forward(layer: e4b.PackedLayer, gate_up: Adapter, down: Adapter, x, ids, gat
     """y bf16 [T, H] and the Kept rows of x bf16 [T, H] with routing ids int32
     and gates fp32 [T, k]."""
     _check(layer, gate_up, down)
-    new = buffers or _fresh
+    with torch.cuda.device(x.device):  # the packed projections run on the current device
+        return _forward(layer, gate_up, down, x, ids, gates, buffers or _fresh)
+
+
+def _forward(layer, gate_up, down, x, ids, gates, new):
     (T, k), dev = ids.shape, x.device
     E, H, I, R = layer.E, layer.H, layer.I, T * k
     bf16 = torch.bfloat16
@@ -135,7 +140,11 @@ def backward(layer: e4b.PackedLayer, gate_up: Adapter, down: Adapter, kept: Kept
     add to)."""
     if accumulate and grads is None:
         raise ValueError("accumulate needs the gradients to add to")
-    new = buffers or _fresh
+    with torch.cuda.device(dy.device):
+        return _backward(layer, gate_up, down, kept, dy, grads, accumulate, buffers or _fresh)
+
+
+def _backward(layer, gate_up, down, kept, dy, grads, accumulate, new):
     (T, k), dev = kept.ids_shape, dy.device
     E, H, I, R = layer.E, layer.H, layer.I, T * k
     bf16, f32 = torch.bfloat16, torch.float32
