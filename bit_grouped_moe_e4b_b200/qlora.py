@@ -117,15 +117,17 @@ def _forward(layer, gate_up, down, x, ids, gates, new):
 
     gu, h = new("gu", (R, 2 * I), bf16, dev), new("h", (R, I), bf16, dev)
     s_gu = new("s_gu", (R, gate_up.a.shape[1]), torch.float32, dev)
-    e4b.e4b_grouped_gemm(layer.fmt, e4b.E4B_EPI_STORE, layer.gate_up_codes, layer.gate_up_scales, xs, offsets, gu, E=E,
-                         N=2 * I, K=H, R_max=R, bias=layer.gate_up_bias)
+    if R:  # the packed projections take no empty batch
+        e4b.e4b_grouped_gemm(layer.fmt, e4b.E4B_EPI_STORE, layer.gate_up_codes, layer.gate_up_scales, xs, offsets, gu, E=E,
+                             N=2 * I, K=H, R_max=R, bias=layer.gate_up_bias)
     e4b.e4b_lora(gate_up.a, gate_up.b, xs, offsets, _lora_ws(gate_up, R, False, new, "ws_gu", dev), base=gu, y=gu, h=h,
                  s=s_gu, scale=gate_up.scale, layout=layer.layout, act=layer.act, alpha=layer.alpha, limit=layer.limit)
 
     ys = new("ys", (R, H), bf16, dev)
     s_dn = new("s_dn", (R, down.a.shape[1]), torch.float32, dev)
-    e4b.e4b_grouped_gemm(layer.fmt, e4b.E4B_EPI_STORE, layer.down_codes, layer.down_scales, h, offsets, ys, E=E, N=H, K=I,
-                         R_max=R, bias=layer.down_bias)
+    if R:
+        e4b.e4b_grouped_gemm(layer.fmt, e4b.E4B_EPI_STORE, layer.down_codes, layer.down_scales, h, offsets, ys, E=E, N=H, K=I,
+                             R_max=R, bias=layer.down_bias)
     e4b.e4b_lora(down.a, down.b, h, offsets, _lora_ws(down, R, False, new, "ws_dn", dev), base=ys, y=ys, s=s_dn,
                  scale=down.scale)
     y = new("y", (T, H), bf16, dev)
@@ -156,7 +158,8 @@ def _backward(layer, gate_up, down, kept, dy, grads, accumulate, new):
     dys, dgates = new("dys", (R, H), bf16, dev), new("dgates", (T, k), f32, dev)
     e4b.e4b_unpermute_backward(dy, kept.ys, kept.inv, kept.gates, dys, dgates, top_k=k)
     dh = new("dh", (R, I), bf16, dev)
-    e4b.e4b_grouped_dgrad(layer.fmt, layer.down_codes, layer.down_scales, dys, kept.offsets, dh, E=E, N=H, K=I, R_max=R)
+    if R:
+        e4b.e4b_grouped_dgrad(layer.fmt, layer.down_codes, layer.down_scales, dys, kept.offsets, dh, E=E, N=H, K=I, R_max=R)
     e4b.e4b_lora_backward(down.a, down.b, kept.h, kept.s_dn, dys, kept.offsets,
                           _lora_ws(down, R, True, new, "ws_ddn", dev), dx=dh, dx_base=dh, da=d_dn.a, db=d_dn.b,
                           accumulate=accumulate, scale=down.scale)
@@ -165,8 +168,9 @@ def _backward(layer, gate_up, down, kept, dy, grads, accumulate, new):
     e4b.e4b_glu_backward(dh, kept.gu, dgu, offsets=kept.offsets, layout=layer.layout, act=layer.act, alpha=layer.alpha,
                          limit=layer.limit)
     dxs = new("dxs", (R, H), bf16, dev)
-    e4b.e4b_grouped_dgrad(layer.fmt, layer.gate_up_codes, layer.gate_up_scales, dgu, kept.offsets, dxs, E=E, N=2 * I,
-                          K=H, R_max=R)
+    if R:
+        e4b.e4b_grouped_dgrad(layer.fmt, layer.gate_up_codes, layer.gate_up_scales, dgu, kept.offsets, dxs, E=E, N=2 * I,
+                              K=H, R_max=R)
     e4b.e4b_lora_backward(gate_up.a, gate_up.b, kept.xs, kept.s_gu, dgu, kept.offsets,
                           _lora_ws(gate_up, R, True, new, "ws_dgu", dev), dx=dxs, dx_base=dxs, da=d_gu.a, db=d_gu.b,
                           accumulate=accumulate, scale=gate_up.scale)

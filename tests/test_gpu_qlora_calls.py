@@ -40,3 +40,17 @@ def test_another_batch_size_between_replays():
     assert all(bool((h == 7.0).all()) for h in held)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert all(torch.equal(a, b) for a, b in zip(step(T // 3), small))
+
+
+def test_a_batch_without_tokens():
+    c = Case(*CASES[2])
+    empty = lambda t: t[:0].cuda().contiguous()  # noqa: E731
+    for buf in (None, qlora.Buffers()):
+        y, kept = qlora.forward(c.layer, *c.dev, empty(c.x), empty(c.ids), empty(c.gates), buf)
+        dx, dgates, gu, dn = qlora.backward(c.layer, *c.dev, kept, empty(c.dy), buffers=buf)
+        assert y.shape == dx.shape == (0, c.layer.H) and dgates.shape == (0, c.ids.shape[1])
+        for t in (gu.a, gu.b, dn.a, dn.b):
+            assert not bool(t.any())
+    grads = tuple(qlora.Gradient(torch.ones_like(d.a), torch.ones_like(d.b)) for d in (gu, dn))
+    qlora.backward(c.layer, *c.dev, kept, empty(c.dy), grads=grads, accumulate=True)
+    assert all(bool((t == 1).all()) for d in grads for t in (d.a, d.b))
