@@ -99,6 +99,9 @@ def forward(layer: e4b.PackedLayer, gate_up: Adapter, down: Adapter, x, ids, gat
     """y bf16 [T, H] and the Kept rows of x bf16 [T, H] with routing ids int32
     and gates fp32 [T, k]."""
     _check(layer, gate_up, down)
+    # the routing pass takes an address: other types would be read as int32
+    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != x.shape[0] or ids.device != x.device:
+        raise ValueError(f"ids: expected int32 [{x.shape[0]}, k] on {x.device}, got {ids.dtype} {tuple(ids.shape)} on {ids.device}")
     with torch.cuda.device(x.device):  # the packed projections run on the current device
         return _forward(layer, gate_up, down, x, ids, gates, buffers or _fresh)
 

@@ -43,3 +43,12 @@ def test_every_call_runs_on_the_tensors_device(calls):
                                      "e4b_lora", "e4b_unpermute"]
     qlora.backward(layer, *ads, kept, torch.zeros_like(x))
     assert len(calls) == 14 and all(d == x.device for _, d in calls)
+
+
+def test_ids_of_another_type_or_batch_are_refused(calls):
+    layer, ads, x, _, gates = inputs()
+    for bad in (torch.zeros(T, K, dtype=torch.int64), torch.zeros(T, K), torch.zeros(T + 1, K, dtype=torch.int32),
+                torch.zeros(T * K, dtype=torch.int32), torch.zeros(T, K, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError, match="ids"):
+            qlora.forward(layer, *ads, x, bad, gates)
+    assert not calls
