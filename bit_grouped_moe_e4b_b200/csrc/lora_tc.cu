@@ -74,7 +74,7 @@ constexpr int kOutChain = 2, kGradChain = 8;     // tiles of eight MMAs
 // where these would leave room for two tiles, hi's and the others'.
 __host__ __device__ constexpr int grad_width(int rp) { return rp <= 32 ? 3 * rp : 2 * rp; }
 constexpr int kMaxStages = 6;
-constexpr int kMaxChunks = 30;                   // column tiles of a block (TMEM: 512 / 16, less two)
+constexpr int kMaxChunks = 512 / grad_width(16); // column tiles of a block whose gradients TMEM holds, at most
 constexpr uint32_t kSmemLimit = 232448;
 
 // A part of a gradient: its group and column block, and whether it is the first
@@ -801,7 +801,6 @@ struct Choices {
   Choices(int rank, int64_t C, bool o, bool g, int n) : r(rank), sms(n), all((C + kTile - 1) / kTile), out(o), grad(g) {
     const int rp = operand_width(rank);
     most = g ? (512 - (o ? 2 * rp : 0)) / grad_width(rp) : 64;
-    if (g && most > kMaxChunks) most = kMaxChunks;
     if (most > all) most = int(all);
   }
   int after(int c) const { return c + (grad || c < 4 ? 1 : c < 16 ? 4 : 16); }
