@@ -531,6 +531,8 @@ e4b_status e4b_unpermute_backward(const uint16_t* dy, int64_t ld_dy, const uint1
  *                     not keep it). The clamps pass a gradient up to and
  *                     including the limit. dgu may be gu (in place); no other
  *                     overlap is allowed.
+ * Computed in fp32, rounded once; a sigmoid below 2^-126 (a gate below about
+ * -87, or -87 / glu_alpha) counts as zero, whatever the up value.
  * I % 8 == 0; strides (in values) multiples of 8, of at least 2I (gu, dgu) and
  * I (h, dh); pointers 16-byte aligned.
  */
