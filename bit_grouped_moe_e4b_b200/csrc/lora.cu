@@ -200,9 +200,11 @@ shrink_kernel(Adapters d, const uint16_t* __restrict__ x, int64_t ld_x, int ksli
 // A operand) are staged in shared memory a tile ahead. Column c of n8-tile i of a
 // strip is the strip's column 8 (c / 2) + 2 i + c % 2, so that a lane's results
 // are eight consecutive columns: one 16-byte access to base, y and h. 8192 rows
-// of 28672 columns, rank 16: 161 us (5.8 TB/s); dx of 4096 columns 21 us; 65536
-// rows of 2 x 768 columns, rank 32, with the activation: about 85 us (3.6 TB/s),
-// there bound by the issue and latency of 16 warps an SM.
+// of 28672 columns, rank 16: about 165 us (5.7 TB/s); dx of 4096 columns 21 us;
+// 65536 rows of 2 x 768 columns, rank 32, with the activation: about 94 us (3.2
+// TB/s), where the 16 warps an SM load, multiply, activate, pack and store in turn.
+// The third term costs 3 and 9 us of these; without it y is off by up to 2^-17 of
+// what base takes away.
 struct Expand {
   const uint16_t* w;
   bool scaled;

@@ -11,9 +11,10 @@
 // same 128B-swizzled boxes), so no thread touches it.
 //
 // Numbers: z and W enter as they are (bf16), sums are fp32 in TMEM. The fp32
-// values v enter as three bf16 terms hi + mid + lo (24 bits of mantissa), which
-// makes the fp32 gradients as exact as fp32 products: two terms left a relative
-// error of 2^-17 a product. The terms lie side by side as columns of one B
+// values v enter as three bf16 terms hi + mid + lo (24 bits of mantissa, one sign:
+// lora_terms.cuh), which makes the fp32 gradients as exact as fp32 products, and
+// infinite where these are: two terms left a relative error of 2^-17 a product. The
+// terms lie side by side as columns of one B
 // operand (N = 3 * rank) up to rank 32, and are added when TMEM is read: three
 // MMAs into one accumulator would read the tile from shared memory, and issue,
 // three times.
