@@ -254,7 +254,8 @@ template <int KS, int GLU>
 constexpr int kStrips = KS > 2 && GLU == kGluNone ? 1 : 2;
 template <int KS, int GLU>
 constexpr int kExpandCtas = KS > 2 && kStrips<KS, GLU> == 2 ? 1 : 2;
-// Sixteens of a tile, at most: above rank 32 with two CTAs an SM the terms of four fit.
+// Sixteens of a tile, at most: above rank 32 with two CTAs an SM the terms of four fit
+// (8192 rows, rank 64, 4096 columns: y 78 us, dx 82; one CTA with eight 106 and 92).
 template <int KS, int GLU>
 constexpr int kSixteens = KS > 2 && kExpandCtas<KS, GLU> == 2 ? 4 : kTile / 16;
 
