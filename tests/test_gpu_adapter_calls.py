@@ -114,3 +114,36 @@ def test_adapters_without_rows():
     assert bool((da == 3.0).all()) and bool((db == 3.0).all())
     e4b.e4b_lora_backward(a, b, x, s, y, off, ws, dx=x, dx_base=x, da=da, db=db)
     assert not bool(da.any()) and not bool(db.any())
+
+
+@pytest.mark.parametrize("mapped", [False, True])
+@pytest.mark.parametrize("r", [16, 64])
+def test_rows_with_strides_on_whole_tiles(r, mapped):
+    # every row buffer with a padding of its own, on another stream; the padding is neither read nor written
+    c = Case([6000, 131, 0, 2000], r, 2312, 520, mapped=mapped, seed=24)
+    assert c.R * c.K * c.r > 2e8  # s on tiles
+    want_f = c.forward()
+    s = c.s()
+    want_b = c.backward(s)
+    pads = []
+
+    def wide(t, pad):
+        whole = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device="cuda")
+        whole[:, :t.shape[1]] = t
+        pads.append(whole[:, t.shape[1]:])
+        return whole[:, :t.shape[1]]
+    x, dy, base, dx_base = wide(c.x, 8), wide(c.dy, 24), wide(c.base, 40), wide(c.dx_base, 16)
+    y, dx = wide(want_f["y"], 56), wide(want_b["dx"], 8)
+    y.fill_(123.0)
+    dx.fill_(123.0)
+    da, db, sf = torch.empty_like(want_b["da"]), torch.empty_like(want_b["db"]), torch.empty_like(want_f["s"])
+    ws = [c.ws(False), c.ws(True)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kw = dict(scale=c.scale, row=c.row, status=c.status, stream=side)
+    e4b.e4b_lora(c.a, c.b, x, c.offsets, ws[0], base=base, y=y, s=sf, **kw)
+    e4b.e4b_lora_backward(c.a, c.b, x, s, dy, c.offsets, ws[1], dx=dx, dx_base=dx_base, da=da, db=db, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want_f["y"]) and torch.equal(dx, want_b["dx"]) and torch.equal(sf[:c.n], want_f["s"][:c.n])
+    assert torch.equal(da, want_b["da"]) and torch.equal(db, want_b["db"])
+    assert all(bool(torch.isnan(p).all()) for p in pads) and int(c.status) == 0
